@@ -343,6 +343,150 @@ spade_status spade_grouped_attn_host(const void* q_host, const void* k_host, con
                                      int text_tokens, spade_dtype dt, int head_chunk,
                                      void* workspace, size_t ws_bytes, spade_stream_t stream);
 
+/* ---- row passes around the attention -----------------------------------------
+ * What a video-DiT layer runs on its token rows right before and after the
+ * attention of this library.  Not from the SPADE pages, which begin at Q/K/V:
+ * the norm and several-axis rotation that make Q and K, and the modulated
+ * norm and gated residual update on either side of a block, each with its
+ * gradient.  Sums, statistics and angles are float32 (angles are reduced in
+ * float64), results are rounded once, to nearest even.
+ *
+ * Rows: every operand is a list of `rows` rows, `stride` elements apart (a
+ * stride at least the row's length; 0 = the row's length, packed), elements
+ * of a row next to one another.  Pointers need the alignment of their type
+ * only.  Rows on 16-byte boundaries, of a multiple of 16 (head channels) or 8
+ * (dim) elements, are read and written 16 bytes at a time; all others run the
+ * same kernels one element at a time.  An output may be the input of the same
+ * row (same pointer and stride) where that is said; otherwise outputs overlap
+ * nothing.  rows = 0 is allowed: nothing is read, parameter gradients become
+ * zero.  Gradients of parameters are float32, added in a fixed order (the same
+ * bits on every run of one device type), and overwritten, not accumulated. */
+
+/* A rotation: pair i turns by position[axis[i]] * freq[i] radians.  Axes are
+ * 0 (t), 1 (y), 2 (x).  Pairs past `pairs` are left as they are (interleaved
+ * style only). */
+#define SPADE_ROPE_MAX_PAIRS 128
+typedef enum {
+  SPADE_ROPE_INTERLEAVED = 0,  /* pair i = channels 2i, 2i + 1      */
+  SPADE_ROPE_HALF = 1          /* pair i = channels i, i + d / 2    */
+} spade_rope_style;
+typedef struct {
+  int32_t pairs, style;
+  int32_t axis[SPADE_ROPE_MAX_PAIRS];
+  double freq[SPADE_ROPE_MAX_PAIRS];
+} spade_rope;
+
+/* Fills `rope` for the usual ladders.  pairs[a] pairs belong to axis a, t
+ * first, then y, then x; pair i of an axis of n pairs has frequency
+ * scale[a] * theta[a]^(-i / n).  shared_ladder = 1: the pairs run down one
+ * ladder of theta[0] over all n = sum of pairs instead, whatever their axis.
+ * Host only. */
+spade_status spade_rope_axes(spade_rope* rope, const int32_t pairs[3], const double theta[3],
+                             const double scale[3], spade_rope_style style, int shared_ladder);
+
+/* RMS norm of Q and K before the rotation: over the token's heads * d values
+ * (weight [heads * d]), over each head's d (weight [d]), or none. */
+typedef enum { SPADE_QK_NORM_NONE = 0, SPADE_QK_NORM_TOKEN = 1, SPADE_QK_NORM_HEAD = 2 } spade_qk_norm;
+
+/* rows         : token rows; the last text_tokens of them are normalised, not
+ *                rotated.
+ * T, H, W      : grid; row r is token token_offset + r of it (all rows but the
+ *                text rows lie inside).  Unused when positions are given.
+ * q_heads, k_heads: 0..128, not both 0; a tensor of 0 heads is absent (NULL).
+ * d            : head channels, even, 2..256; rope->pairs <= d / 2, and = d / 2
+ *                in the half style.
+ * *_stride     : x: q, k.  out: q_out, k_out (backward: dq, dk).  dout: the
+ *                incoming gradients (backward only). */
+typedef struct {
+  int64_t rows, text_tokens, token_offset;
+  int32_t T, H, W;
+  int32_t q_heads, k_heads, d;
+  int32_t dt, weight_dt;       /* spade_dtype */
+  int32_t norm;                /* spade_qk_norm */
+  float eps;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride, q_dout_stride, k_dout_stride;
+} spade_qk_desc;
+
+/* q_out = rotate(norm(q)), k_out likewise, in one pass.  positions: device
+ * int32 [rows, 3] (t, y, x of each row, any int32), or NULL for the grid
+ * (with positions text_tokens must be 0).  Weights may be NULL (ones).
+ * q_out / k_out may be q / k. */
+spade_status spade_qk_norm_rope(const spade_qk_desc* desc, const spade_rope* rope, const int32_t* positions,
+                                const void* q, const void* k, const void* q_weight, const void* k_weight,
+                                void* q_out, void* k_out, spade_stream_t stream);
+
+/* Its gradient: dq, dk (of q, k) from dq_out, dk_out; q and k are the forward
+ * call's inputs (unused, may be NULL, without a norm).  dq_weight, dk_weight:
+ * float32, or NULL.  dq / dk may be dq_out / dk_out.  workspace: device scratch of
+ * spade_qk_norm_rope_bwd_workspace_bytes() bytes (0 without a norm), asked for
+ * with the device of the call current. */
+size_t spade_qk_norm_rope_bwd_workspace_bytes(const spade_qk_desc* desc);
+spade_status spade_qk_norm_rope_bwd(const spade_qk_desc* desc, const spade_rope* rope, const int32_t* positions,
+                                    const void* dq_out, const void* dk_out, const void* q, const void* k,
+                                    const void* q_weight, const void* k_weight, void* dq, void* dk,
+                                    float* dq_weight, float* dk_weight, void* workspace, size_t ws_bytes,
+                                    spade_stream_t stream);
+
+typedef enum { SPADE_NORM_NONE = 0, SPADE_NORM_RMS = 1, SPADE_NORM_LAYER = 2 } spade_norm;
+
+/* rows         : split evenly into `groups` runs of consecutive rows; group g
+ *                uses row g of gate, scale and shift (1: one modulation for
+ *                all; the number of frames or samples; rows: one per token).
+ * dim          : 1..16384.
+ * x_dt         : residual stream (x, x_out, dx, dx_out); branch_dt: y, h, dy,
+ *                dh.  Pairs: f32/f32, f32/bf16, bf16/bf16.
+ * param_dt     : gate, post_weight, weight, bias, scale, shift.
+ * norm         : RMS or LAYER (population variance); post_norm may be NONE. */
+typedef struct {
+  int64_t rows, groups;
+  int32_t dim;
+  int32_t x_dt, branch_dt, param_dt;   /* spade_dtype */
+  int32_t norm, post_norm;             /* spade_norm */
+  float eps, post_eps, residual_scale;
+  int64_t x_stride, y_stride, x_out_stride, h_stride;
+  int64_t dx_out_stride, dh_stride, dx_stride, dy_stride;
+  int64_t gate_stride, scale_stride, shift_stride;
+} spade_row_desc;
+
+/* Device parameters, each NULL for the identity: weight, bias, post_weight
+ * [dim]; gate, scale, shift [groups, dim] with their strides. */
+typedef struct { const void *gate, *post_weight, *weight, *bias, *scale, *shift; } spade_row_params;
+/* Device float32 gradients of the same, packed, each NULL if not wanted. */
+typedef struct { float *gate, *post_weight, *weight, *bias, *scale, *shift; } spade_row_grads;
+
+/* h = (norm(x) * weight + bias) * (1 + scale) + shift.  h may be x when both
+ * have one type. */
+spade_status spade_norm_modulate(const spade_row_desc* desc, const spade_row_params* params, const void* x, void* h,
+                                 spade_stream_t stream);
+/* x_out = x + residual_scale * gate * (post_norm(y) * post_weight).  x_out may
+ * be x, or y when both have one type. */
+spade_status spade_gate_residual(const spade_row_desc* desc, const spade_row_params* params, const void* x,
+                                 const void* y, void* x_out, spade_stream_t stream);
+/* Both in one pass: x_out as spade_gate_residual, h = spade_norm_modulate of
+ * the sum before its rounding to x_dt.  x_out may be x; h may be y. */
+spade_status spade_gate_residual_norm(const spade_row_desc* desc, const spade_row_params* params, const void* x,
+                                      const void* y, void* x_out, void* h, spade_stream_t stream);
+
+/* Gradients.  workspace: device scratch of spade_row_bwd_workspace_bytes()
+ * bytes, asked for with the device of the call current.
+ * spade_norm_modulate_bwd: dx = dres + the gradient through the norm; dres
+ * (stride dx_out_stride) is a gradient that reaches x by another way, or NULL.
+ * spade_gate_residual_bwd: dy from dx_out (the gradient of x is dx_out).
+ * spade_gate_residual_norm_bwd: dx and dy from dx_out (NULL: x_out unused) and
+ * dh, with x and y the forward call's inputs.
+ * dx may be dx_out or dres; dy may be dh or y. */
+size_t spade_row_bwd_workspace_bytes(const spade_row_desc* desc);
+spade_status spade_norm_modulate_bwd(const spade_row_desc* desc, const spade_row_params* params, const void* dh,
+                                     const void* dres, const void* x, void* dx, const spade_row_grads* grads,
+                                     void* workspace, size_t ws_bytes, spade_stream_t stream);
+spade_status spade_gate_residual_bwd(const spade_row_desc* desc, const spade_row_params* params, const void* dx_out,
+                                     const void* y, void* dy, const spade_row_grads* grads, void* workspace,
+                                     size_t ws_bytes, spade_stream_t stream);
+spade_status spade_gate_residual_norm_bwd(const spade_row_desc* desc, const spade_row_params* params,
+                                          const void* dx_out, const void* dh, const void* x, const void* y, void* dx,
+                                          void* dy, const spade_row_grads* grads, void* workspace, size_t ws_bytes,
+                                          spade_stream_t stream);
+
 /* ---- status ---------------------------------------------------------------
  * spade_last_device_status synchronises `stream`, returns the latched device
  * status (SPADE_OK or SPADE_ERR_TIMEOUT) and clears it. */

@@ -24,6 +24,44 @@ class SpadeHeadScheme(ctypes.Structure):
     _fields_ = [("scheme", c_int32), ("tau", c_float), ("dense", c_int32)]
 
 
+ROPE_MAX_PAIRS = 128
+ROPE_STYLE = {"interleaved": 0, "half": 1}
+QK_NORM = {"none": 0, "token": 1, "head": 2}
+NORM = {"none": 0, "rms": 1, "layer": 2}
+
+
+class SpadeRope(ctypes.Structure):
+    _fields_ = [("pairs", c_int32), ("style", c_int32), ("axis", c_int32 * ROPE_MAX_PAIRS),
+                ("freq", ctypes.c_double * ROPE_MAX_PAIRS)]
+
+
+class SpadeQkDesc(ctypes.Structure):
+    _fields_ = ([(n, c_int64) for n in ("rows", "text_tokens", "token_offset")] +
+                [(n, c_int32) for n in ("T", "H", "W", "q_heads", "k_heads", "d", "dt", "weight_dt", "norm")] +
+                [("eps", c_float)] +
+                [(n, c_int64) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride", "q_dout_stride",
+                                        "k_dout_stride")])
+
+
+class SpadeRowDesc(ctypes.Structure):
+    _fields_ = ([("rows", c_int64), ("groups", c_int64)] +
+                [(n, c_int32) for n in ("dim", "x_dt", "branch_dt", "param_dt", "norm", "post_norm")] +
+                [(n, c_float) for n in ("eps", "post_eps", "residual_scale")] +
+                [(n, c_int64) for n in ("x_stride", "y_stride", "x_out_stride", "h_stride", "dx_out_stride", "dh_stride",
+                                        "dx_stride", "dy_stride", "gate_stride", "scale_stride", "shift_stride")])
+
+
+ROW_PARAMS = ("gate", "post_weight", "weight", "bias", "scale", "shift")
+
+
+class SpadeRowParams(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ROW_PARAMS]
+
+
+class SpadeRowGrads(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ROW_PARAMS]
+
+
 # name -> (restype, argtypes), in the order of include/spade.h
 SIGNATURES = {
     "spade_tile3d": (c_int, [c_void_p, c_void_p, SpadeGeom, c_int, c_int, c_int, c_void_p]),
@@ -66,6 +104,22 @@ SIGNATURES = {
     "spade_grouped_attn_host": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, POINTER(SpadeGeom), c_int,
                                         POINTER(SpadeHeadScheme), c_int, c_int, c_int, c_int, c_int, c_void_p,
                                         c_size_t, c_void_p]),
+    "spade_rope_axes": (c_int, [POINTER(SpadeRope), POINTER(c_int32), POINTER(ctypes.c_double),
+                                POINTER(ctypes.c_double), c_int, c_int]),
+    "spade_qk_norm_rope": (c_int, [POINTER(SpadeQkDesc), POINTER(SpadeRope)] + [c_void_p] * 8),
+    "spade_qk_norm_rope_bwd_workspace_bytes": (c_size_t, [POINTER(SpadeQkDesc)]),
+    "spade_qk_norm_rope_bwd": (c_int, [POINTER(SpadeQkDesc), POINTER(SpadeRope)] + [c_void_p] * 12 +
+                               [c_size_t, c_void_p]),
+    "spade_norm_modulate": (c_int, [POINTER(SpadeRowDesc), POINTER(SpadeRowParams)] + [c_void_p] * 3),
+    "spade_gate_residual": (c_int, [POINTER(SpadeRowDesc), POINTER(SpadeRowParams)] + [c_void_p] * 4),
+    "spade_gate_residual_norm": (c_int, [POINTER(SpadeRowDesc), POINTER(SpadeRowParams)] + [c_void_p] * 5),
+    "spade_row_bwd_workspace_bytes": (c_size_t, [POINTER(SpadeRowDesc)]),
+    "spade_norm_modulate_bwd": (c_int, [POINTER(SpadeRowDesc), POINTER(SpadeRowParams)] + [c_void_p] * 4 +
+                                [POINTER(SpadeRowGrads), c_void_p, c_size_t, c_void_p]),
+    "spade_gate_residual_bwd": (c_int, [POINTER(SpadeRowDesc), POINTER(SpadeRowParams)] + [c_void_p] * 3 +
+                                [POINTER(SpadeRowGrads), c_void_p, c_size_t, c_void_p]),
+    "spade_gate_residual_norm_bwd": (c_int, [POINTER(SpadeRowDesc), POINTER(SpadeRowParams)] + [c_void_p] * 6 +
+                                     [POINTER(SpadeRowGrads), c_void_p, c_size_t, c_void_p]),
     "spade_last_device_status": (c_int, [c_void_p]),
     "spade_status_string": (ctypes.c_char_p, [c_int]),
     "spade_last_error_message": (ctypes.c_char_p, []),

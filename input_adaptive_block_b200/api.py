@@ -7,12 +7,13 @@ arithmetic happens in its CUDA kernels.  PyTorch provides memory and streams.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
 from . import _lib
-from ._lib import SpadeGeom, SpadeHeadScheme, check
+from ._lib import (NORM, QK_NORM, ROPE_STYLE, ROW_PARAMS, SpadeGeom, SpadeHeadScheme, SpadeQkDesc, SpadeRope,
+                   SpadeRowDesc, SpadeRowGrads, SpadeRowParams, check)
 
 __all__ = [
     "geom", "dtype_code", "tile3d", "summarize", "summarize_qk", "estimate", "estimate_scores", "select", "select_scores",
@@ -20,6 +21,9 @@ __all__ = [
     "block_sparse_attn", "block_sparse_attn_noalloc", "grouped_workspace_bytes", "grouped_attn", "grouped_head_lists",
     "last_device_status", "selftest_bounded_wait", "num_blocks", "sics_workspace_bytes", "sics", "select_window",
     "grouped_attn_from_host", "grouped_host_workspace_bytes", "grouped_attn_lists",
+    "rope_axes", "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_workspace_bytes", "QkGrads",
+    "norm_modulate", "norm_modulate_backward", "gate_residual", "gate_residual_backward", "gate_residual_norm",
+    "gate_residual_norm_backward", "row_workspace_bytes", "RowGrads",
 ]
 
 
@@ -321,6 +325,440 @@ def sics(q: torch.Tensor, k: torch.Tensor, candidates, workspace: Optional[torch
                                  _dev(scores, "scores"), _dev(choice, "choice"), _dev(workspace, "workspace"),
                                  workspace.numel(), _stream(stream)), "spade_sics")
     return scores, choice
+
+
+# ---- row passes around the attention ----------------------------------------
+def rope_axes(d: int, pairs: Sequence[int], theta=10000.0, scale=1.0, style: str = "interleaved",
+              shared_ladder: bool = False) -> SpadeRope:
+    """The rotation of heads of d channels over the axes (t, y, x): pairs[a]
+    pairs turn with axis a, at frequencies scale[a] * theta[a]^(-i / pairs[a])
+    (theta, scale: one number or one per axis), or down one ladder over all
+    pairs (shared_ladder).  style: "interleaved" pairs channels 2i, 2i + 1;
+    "half" pairs i, i + d / 2.  A plan: make it once, pass it to every call."""
+    per_axis = lambda v: [float(x) for x in v] if hasattr(v, "__len__") else [float(v)] * 3  # noqa: E731
+    th, sc = per_axis(theta), per_axis(scale)
+    if len(pairs) != 3 or len(th) != 3 or len(sc) != 3:
+        raise ValueError("pairs, theta and scale have one entry per axis (t, y, x)")
+    if 2 * sum(int(p) for p in pairs) > d:
+        raise ValueError(f"{sum(pairs)} pairs in heads of {d} channels")
+    rope = SpadeRope()
+    check(_lib.load().spade_rope_axes(ctypes.byref(rope), (ctypes.c_int32 * 3)(*[int(p) for p in pairs]),
+                                      (ctypes.c_double * 3)(*th), (ctypes.c_double * 3)(*sc),
+                                      _code(ROPE_STYLE, style, "style"),
+                                      int(bool(shared_ladder))), "spade_rope_axes")
+    return rope
+
+
+class QkGrads(NamedTuple):
+    """Gradients of qk_norm_rope: of its inputs, and of the weights given."""
+    q: Optional[torch.Tensor]
+    k: Optional[torch.Tensor]
+    q_weight: Optional[torch.Tensor]
+    k_weight: Optional[torch.Tensor]
+
+
+class RowGrads(NamedTuple):
+    """Gradients of a row pass: of its inputs, and of the parameters given."""
+    x: Optional[torch.Tensor]
+    y: Optional[torch.Tensor]
+    weight: Optional[torch.Tensor]
+    bias: Optional[torch.Tensor]
+    scale: Optional[torch.Tensor]
+    shift: Optional[torch.Tensor]
+    gate: Optional[torch.Tensor]
+    post_weight: Optional[torch.Tensor]
+
+
+class _On:
+    """Makes `like`'s device and, when given, `stream` current for a call, so
+    that what it allocates belongs to the stream it runs on."""
+
+    def __init__(self, like: torch.Tensor, stream):
+        if stream is not None and stream.device != like.device:
+            raise ValueError(f"stream of {stream.device} for tensors of {like.device}")
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != like.device.index:
+            self.ctx = torch.cuda.device(like.device)
+        else:
+            self.ctx = None
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc) if self.ctx is not None else None
+
+
+def _on_gpu(t: torch.Tensor, name: str, like: torch.Tensor) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+def _strided(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dtype) -> Tuple[Optional[int], int]:
+    """(pointer, row stride) of a tensor of rows [rows, ...] whose rows are
+    packed inside and may lie any distance apart."""
+    if t is None:
+        return None, 0
+    _on_gpu(t, name, like)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
+    inner = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != inner:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        inner *= size
+    if t.shape[0] <= 1 or inner == 0:
+        return t.data_ptr(), 0
+    if t.stride(0) < inner:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.data_ptr(), t.stride(0)
+
+
+def _vector(t: Optional[torch.Tensor], name: str, like: torch.Tensor, n: int, dtype) -> Optional[int]:
+    if t is None:
+        return None
+    _on_gpu(t, name, like)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous elements")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
+    return t.data_ptr()
+
+
+def _param_dtype(params) -> torch.dtype:
+    given = [t.dtype for t in params if t is not None]
+    if any(dt != given[0] for dt in given):
+        raise TypeError(f"parameters of several dtypes: {given}")
+    return given[0] if given else torch.float32
+
+
+def _scratch(workspace, need: int, like: torch.Tensor) -> Tuple[Optional[int], int, Optional[torch.Tensor]]:
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    _on_gpu(workspace, "workspace", like)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _code(table, key, name: str) -> int:
+    if key not in table:
+        raise ValueError(f"{name}={key!r} (one of {', '.join(table)})")
+    return table[key]
+
+
+def _qk_desc(q, k, q_weight, k_weight, grid, positions, token_offset, text_tokens, norm, eps):
+    like = q if q is not None else k
+    if like is None:
+        raise ValueError("neither q nor k")
+    _on_gpu(like, "q" if q is not None else "k", like)
+    if like.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != like.shape[0] or k.shape[2] != like.shape[2])):
+        raise ValueError("q and k are [rows, heads, d]")
+    rows, _, d = like.shape
+    desc = SpadeQkDesc()
+    desc.rows, desc.text_tokens, desc.token_offset = rows, int(text_tokens), int(token_offset)
+    desc.q_heads, desc.k_heads, desc.d = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], d
+    wdt = _param_dtype((q_weight, k_weight))
+    desc.dt, desc.weight_dt = dtype_code(like.dtype), dtype_code(wdt)
+    desc.norm, desc.eps = _code(QK_NORM, norm, "norm"), eps
+    pos = None
+    if positions is not None:
+        if grid is not None or token_offset:
+            raise ValueError("positions and a grid")
+        if positions.dtype != torch.int32:
+            raise TypeError(f"positions has dtype {positions.dtype}, not torch.int32")
+        if tuple(positions.shape) != (rows, 3) or not positions.is_contiguous():
+            raise ValueError(f"positions must be contiguous [{rows}, 3]")
+        _on_gpu(positions, "positions", like)
+        pos = positions.data_ptr()
+    elif grid is not None:
+        g = grid if isinstance(grid, SpadeGeom) else None
+        t = (g.T, g.H, g.W) if g is not None else (grid.as_tuple() if hasattr(grid, "as_tuple") else tuple(grid))
+        desc.T, desc.H, desc.W = int(t[0]), int(t[1]), int(t[2])
+    elif rows > text_tokens:
+        raise ValueError("neither positions nor a grid")
+    per = lambda t: 0 if t is None else (t.shape[1] * d if norm == "token" else d)  # noqa: E731
+    weights = (_vector(q_weight, "q_weight", like, per(q), wdt), _vector(k_weight, "k_weight", like, per(k), wdt))
+    return desc, like, pos, weights
+
+
+def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: SpadeRope, grid=None,
+                 positions: Optional[torch.Tensor] = None, token_offset: int = 0, text_tokens: int = 0,
+                 norm: str = "none", q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, stream=None):
+    """Q and K ready for the attention, in one pass: rms norm (norm "token":
+    over heads * d, "head": over d, "none") times weight, then the rotation.
+
+    q [rows, q_heads, d], k [rows, k_heads, d] (either may be None); rows may
+    lie apart, as in slices of one QKV projection.  Row r stands at token
+    token_offset + r of grid (T, H, W) (a blocking scheme does too), its last
+    text_tokens rows are text and not rotated; or at positions[r] (int32
+    [rows, 3], t y x).  q_out / k_out: where the results go (q and k
+    themselves are allowed), packed tensors by default.  Returns (q_out,
+    k_out)."""
+    desc, like, pos, (qw, kw) = _qk_desc(q, k, q_weight, k_weight, grid, positions, token_offset, text_tokens, norm, eps)
+    with _On(like, stream) as s:
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        rows, d, dt = desc.rows, desc.d, like.dtype
+        qs, ks = (rows, desc.q_heads, d), (rows, desc.k_heads, d)
+        qp, desc.q_stride = _strided(q, "q", like, qs, dt)
+        kp, desc.k_stride = _strided(k, "k", like, ks, dt)
+        qo, desc.q_out_stride = _strided(q_out if q is not None else None, "q_out", like, qs, dt)
+        ko, desc.k_out_stride = _strided(k_out if k is not None else None, "k_out", like, ks, dt)
+        check(_lib.load().spade_qk_norm_rope(ctypes.byref(desc), ctypes.byref(rope), pos, qp, kp, qw, kw, qo, ko, s),
+              "spade_qk_norm_rope")
+    return (q_out if q is not None else None), (k_out if k is not None else None)
+
+
+def qk_norm_rope_workspace_bytes(rows: int, q_heads: int, k_heads: int, d: int, norm: str) -> int:
+    """Scratch of qk_norm_rope_backward on the current device."""
+    desc = SpadeQkDesc(rows=rows, q_heads=q_heads, k_heads=k_heads, d=d, norm=_code(QK_NORM, norm, "norm"))
+    return int(_lib.load().spade_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
+                          k: Optional[torch.Tensor], rope: SpadeRope, grid=None,
+                          positions: Optional[torch.Tensor] = None, token_offset: int = 0, text_tokens: int = 0,
+                          norm: str = "none", q_weight: Optional[torch.Tensor] = None,
+                          k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> QkGrads:
+    """Gradients of qk_norm_rope's inputs and of the weights given (float32),
+    from those of its results.  q and k are that call's inputs (with norm
+    "none" they may be None).  dq / dk: where the gradients go (dq_out and
+    dk_out themselves are allowed)."""
+    desc, like, pos, (qw, kw) = _qk_desc(dq_out, dk_out, q_weight, k_weight, grid, positions, token_offset, text_tokens,
+                                         norm, eps)
+    with _On(like, stream) as s:
+        rows, d, dt = desc.rows, desc.d, like.dtype
+        qs, ks = (rows, desc.q_heads, d), (rows, desc.k_heads, d)
+        if dq_out is not None and dq is None:
+            dq = torch.empty(qs, dtype=dt, device=like.device)
+        if dk_out is not None and dk is None:
+            dk = torch.empty(ks, dtype=dt, device=like.device)
+        gq, desc.q_dout_stride = _strided(dq_out, "dq_out", like, qs, dt)
+        gk, desc.k_dout_stride = _strided(dk_out, "dk_out", like, ks, dt)
+        normed = norm != "none"
+        qp, desc.q_stride = _strided(q if normed and dq_out is not None else None, "q", like, qs, dt)
+        kp, desc.k_stride = _strided(k if normed and dk_out is not None else None, "k", like, ks, dt)
+        qo, desc.q_out_stride = _strided(dq if dq_out is not None else None, "dq", like, qs, dt)
+        ko, desc.k_out_stride = _strided(dk if dk_out is not None else None, "dk", like, ks, dt)
+        dqw, dkw = (None if w is None else torch.empty(w.shape, dtype=torch.float32, device=like.device)
+                    for w in (q_weight, k_weight))
+        lib = _lib.load()
+        need = int(lib.spade_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(desc))) if dqw is not None or dkw is not None else 0
+        wp, wn, workspace = _scratch(workspace, need, like)
+        check(lib.spade_qk_norm_rope_bwd(ctypes.byref(desc), ctypes.byref(rope), pos, gq, gk, qp, kp, qw, kw, qo, ko,
+                                         dqw.data_ptr() if dqw is not None else None,
+                                         dkw.data_ptr() if dkw is not None else None, wp, wn, s),
+              "spade_qk_norm_rope_bwd")
+    return QkGrads(dq if dq_out is not None else None, dk if dk_out is not None else None, dqw, dkw)
+
+
+def _row_call(like, x_dtype, branch_dtype, norm="none", eps=0.0, post_norm="none", post_eps=0.0, residual_scale=1.0,
+              gate=None, post_weight=None, weight=None, bias=None, scale=None, shift=None):
+    """Descriptor and parameters of a row pass over `like` [rows, dim]."""
+    _on_gpu(like, "x", like)
+    if like.dim() != 2:
+        raise ValueError("rows are [rows, dim]")
+    rows, dim = like.shape
+    desc, params = SpadeRowDesc(), SpadeRowParams()
+    given = {"gate": gate, "post_weight": post_weight, "weight": weight, "bias": bias, "scale": scale, "shift": shift}
+    pdt = _param_dtype(given.values())
+    groups = None
+    for name in ("gate", "scale", "shift"):
+        t = given[name]
+        if t is None:
+            continue
+        if t.dim() not in (1, 2) or t.shape[-1] != dim:
+            raise ValueError(f"{name} must be [groups, {dim}] or [{dim}]")
+        g = t.shape[0] if t.dim() == 2 else 1
+        if groups not in (None, g):
+            raise ValueError("gate, scale and shift must have one number of groups")
+        groups = g
+        p, stride = _strided(t if t.dim() == 2 else t.unsqueeze(0), name, like, (g, dim), pdt)
+        setattr(params, name, p)
+        setattr(desc, name + "_stride", stride)
+    groups = 1 if groups is None else groups
+    if groups < 1 or rows % groups:
+        raise ValueError(f"{rows} rows in {groups} groups")
+    for name in ("post_weight", "weight", "bias"):
+        setattr(params, name, _vector(given[name], name, like, dim, pdt))
+    desc.rows, desc.groups, desc.dim = rows, groups, dim
+    desc.x_dt, desc.branch_dt, desc.param_dt = dtype_code(x_dtype), dtype_code(branch_dtype), dtype_code(pdt)
+    desc.norm, desc.post_norm = _code(NORM, norm, "norm"), _code(NORM, post_norm, "post_norm")
+    desc.eps, desc.post_eps, desc.residual_scale = eps, post_eps, residual_scale
+    return desc, params, given
+
+
+def _row_grads(given, like):
+    """Float32 gradient tensors of the parameters given, and their table."""
+    out = {n: None if given[n] is None else torch.empty(given[n].shape, dtype=torch.float32, device=like.device)
+           for n in ROW_PARAMS}
+    return out, SpadeRowGrads(**{n: None if t is None else t.data_ptr() for n, t in out.items()})
+
+
+def row_workspace_bytes(rows: int, dim: int, groups: int = 1) -> int:
+    """Scratch of norm_modulate_backward, gate_residual_backward and
+    gate_residual_norm_backward on the current device."""
+    desc = SpadeRowDesc(rows=rows, groups=groups, dim=dim)
+    return int(_lib.load().spade_row_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def norm_modulate(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None, norm: str = "layer",
+                  eps: float = 1e-6, out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                  stream=None) -> torch.Tensor:
+    """The norm that opens a block: (norm(x) * weight + bias) * (1 + scale) +
+    shift, each parameter optional.  x [rows, dim]; weight, bias [dim]; scale,
+    shift [groups, dim] (or [dim]): the rows fall into `groups` equal runs
+    (frames, samples, or single tokens).  norm: "layer" or "rms".  The result
+    is out, or a new tensor of out_dtype (x's by default)."""
+    odt = out.dtype if out is not None else (out_dtype or x.dtype)
+    desc, params, _ = _row_call(x, x.dtype, odt, norm, eps, weight=weight, bias=bias, scale=scale, shift=shift)
+    with _On(x, stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=odt, device=x.device)
+        xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
+        op, desc.h_stride = _strided(out, "out", x, x.shape, odt)
+        check(_lib.load().spade_norm_modulate(ctypes.byref(desc), ctypes.byref(params), xp, op, s), "spade_norm_modulate")
+    return out
+
+
+def norm_modulate_backward(dout: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                           bias: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                           shift: Optional[torch.Tensor] = None, norm: str = "layer", eps: float = 1e-6,
+                           dres: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> RowGrads:
+    """Gradients of norm_modulate: of x (plus dres, a gradient that reaches x
+    by another way) and of the parameters given (float32).  dx: where x's goes
+    (dres itself is allowed)."""
+    desc, params, given = _row_call(x, x.dtype, dout.dtype, norm, eps, weight=weight, bias=bias, scale=scale, shift=shift)
+    with _On(x, stream) as s:
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
+        hp, desc.dh_stride = _strided(dout, "dout", x, x.shape, dout.dtype)
+        rp, desc.dx_out_stride = _strided(dres, "dres", x, x.shape, x.dtype)
+        dp, desc.dx_stride = _strided(dx, "dx", x, x.shape, x.dtype)
+        out, grads = _row_grads(given, x)
+        lib = _lib.load()
+        wp, wn, workspace = _scratch(workspace, int(lib.spade_row_bwd_workspace_bytes(ctypes.byref(desc))), x)
+        check(lib.spade_norm_modulate_bwd(ctypes.byref(desc), ctypes.byref(params), hp, rp, xp, dp, ctypes.byref(grads),
+                                          wp, wn, s), "spade_norm_modulate_bwd")
+    return RowGrads(x=dx, y=None, **out)
+
+
+def gate_residual(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor] = None, post_norm: str = "none",
+                  post_weight: Optional[torch.Tensor] = None, post_eps: float = 1e-6, residual_scale: float = 1.0,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The update that ends a block: x + residual_scale * gate *
+    (post_norm(y) * post_weight).  x, y [rows, dim]; gate [groups, dim] or
+    [dim].  out: where the sum goes (x itself is allowed)."""
+    desc, params, _ = _row_call(x, x.dtype, y.dtype, post_norm=post_norm, post_eps=post_eps,
+                                residual_scale=residual_scale, gate=gate, post_weight=post_weight)
+    with _On(x, stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
+        yp, desc.y_stride = _strided(y, "y", x, x.shape, y.dtype)
+        op, desc.x_out_stride = _strided(out, "out", x, x.shape, x.dtype)
+        check(_lib.load().spade_gate_residual(ctypes.byref(desc), ctypes.byref(params), xp, yp, op, s),
+              "spade_gate_residual")
+    return out
+
+
+def gate_residual_backward(dout: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                           post_norm: str = "none", post_weight: Optional[torch.Tensor] = None,
+                           post_eps: float = 1e-6, residual_scale: float = 1.0, dy: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> RowGrads:
+    """Gradients of gate_residual: of y and of the parameters given (float32).
+    x's gradient is dout (returned as x)."""
+    desc, params, given = _row_call(dout, dout.dtype, y.dtype, post_norm=post_norm, post_eps=post_eps,
+                                    residual_scale=residual_scale, gate=gate, post_weight=post_weight)
+    with _On(dout, stream) as s:
+        if dy is None:
+            dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        gp, desc.dx_out_stride = _strided(dout, "dout", dout, dout.shape, dout.dtype)
+        yp, desc.y_stride = _strided(y, "y", dout, dout.shape, y.dtype)
+        dp, desc.dy_stride = _strided(dy, "dy", dout, dout.shape, y.dtype)
+        out, grads = _row_grads(given, dout)
+        lib = _lib.load()
+        wp, wn, workspace = _scratch(workspace, int(lib.spade_row_bwd_workspace_bytes(ctypes.byref(desc))), dout)
+        check(lib.spade_gate_residual_bwd(ctypes.byref(desc), ctypes.byref(params), gp, yp, dp, ctypes.byref(grads), wp,
+                                          wn, s), "spade_gate_residual_bwd")
+    return RowGrads(x=dout, y=dy, **out)
+
+
+def gate_residual_norm(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor] = None, post_norm: str = "none",
+                       post_weight: Optional[torch.Tensor] = None, post_eps: float = 1e-6,
+                       residual_scale: float = 1.0, weight: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                       shift: Optional[torch.Tensor] = None, norm: str = "layer", eps: float = 1e-6,
+                       x_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """gate_residual and the norm_modulate of the block that follows, in one
+    pass: returns (x_out, out), out of y's dtype, taken of the sum before it
+    is rounded to x's.  x_out may be x, out may be y."""
+    desc, params, _ = _row_call(x, x.dtype, y.dtype, norm, eps, post_norm, post_eps, residual_scale, gate, post_weight,
+                                weight, bias, scale, shift)
+    with _On(x, stream) as s:
+        if x_out is None:
+            x_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if out is None:
+            out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
+        yp, desc.y_stride = _strided(y, "y", x, x.shape, y.dtype)
+        op, desc.x_out_stride = _strided(x_out, "x_out", x, x.shape, x.dtype)
+        hp, desc.h_stride = _strided(out, "out", x, x.shape, y.dtype)
+        check(_lib.load().spade_gate_residual_norm(ctypes.byref(desc), ctypes.byref(params), xp, yp, op, hp, s),
+              "spade_gate_residual_norm")
+    return x_out, out
+
+
+def gate_residual_norm_backward(dx_out: Optional[torch.Tensor], dout: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
+                                gate: Optional[torch.Tensor] = None, post_norm: str = "none",
+                                post_weight: Optional[torch.Tensor] = None, post_eps: float = 1e-6,
+                                residual_scale: float = 1.0, weight: Optional[torch.Tensor] = None,
+                                bias: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                                shift: Optional[torch.Tensor] = None, norm: str = "layer", eps: float = 1e-6,
+                                dx: Optional[torch.Tensor] = None, dy: Optional[torch.Tensor] = None,
+                                workspace: Optional[torch.Tensor] = None, stream=None) -> RowGrads:
+    """Gradients of gate_residual_norm: of x and y (its inputs, given again)
+    and of the parameters given (float32), from those of x_out (None: unused)
+    and out.  dx may be dx_out; dy may be dout."""
+    desc, params, given = _row_call(x, x.dtype, y.dtype, norm, eps, post_norm, post_eps, residual_scale, gate, post_weight,
+                                    weight, bias, scale, shift)
+    with _On(x, stream) as s:
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if dy is None:
+            dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        gp, desc.dx_out_stride = _strided(dx_out, "dx_out", x, x.shape, x.dtype)
+        hp, desc.dh_stride = _strided(dout, "dout", x, x.shape, y.dtype)
+        xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
+        yp, desc.y_stride = _strided(y, "y", x, x.shape, y.dtype)
+        dxp, desc.dx_stride = _strided(dx, "dx", x, x.shape, x.dtype)
+        dyp, desc.dy_stride = _strided(dy, "dy", x, x.shape, y.dtype)
+        out, grads = _row_grads(given, x)
+        lib = _lib.load()
+        wp, wn, workspace = _scratch(workspace, int(lib.spade_row_bwd_workspace_bytes(ctypes.byref(desc))), x)
+        check(lib.spade_gate_residual_norm_bwd(ctypes.byref(desc), ctypes.byref(params), gp, hp, xp, yp, dxp, dyp,
+                                               ctypes.byref(grads), wp, wn, s), "spade_gate_residual_norm_bwd")
+    return RowGrads(x=dx, y=dy, **out)
 
 
 def last_device_status(stream=None) -> int:

@@ -3,6 +3,7 @@
 // single steps and for the grouped (mixed-scheme) layer.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -331,6 +332,414 @@ cudaError_t host_pipe_setup(HostPipe& P, size_t n_events) {
     P.ev.push_back(ev);
   }
   return cudaSuccess;
+}
+
+// ---- row passes around the attention: checks of their operands ----
+
+constexpr long long kMaxRows = 1LL << 40;
+
+// A list of rows in memory, for the overlap checks (bytes).
+struct Region {
+  const char* name;
+  uintptr_t p;
+  unsigned long long rows, stride, len;
+  bool out, row;      // written; token rows (not a parameter, a gradient of one, or scratch)
+};
+
+struct Regions {
+  Region r[24];
+  int n = 0;
+  void add(const char* name, const void* p, long long rows, long long stride, long long len, bool out,
+           bool row = false) {
+    if (p && rows > 0 && len > 0)
+      r[n++] = {name, reinterpret_cast<uintptr_t>(p), (unsigned long long)rows, (unsigned long long)stride,
+                (unsigned long long)len, out, row};
+  }
+};
+
+bool disjoint(const Region& a, const Region& b) {
+  const uintptr_t ae = a.p + (a.rows - 1) * a.stride + a.len, be = b.p + (b.rows - 1) * b.stride + b.len;
+  if (ae <= b.p || be <= a.p) return true;
+  if (a.rows == 1 || b.rows == 1 || a.stride != b.stride) return false;
+  // rows of one spacing: b's rows start `gap` bytes into a's spacing
+  const unsigned long long gap = b.p >= a.p ? (b.p - a.p) % a.stride : (a.stride - (a.p - b.p) % a.stride) % a.stride;
+  return gap >= a.len && gap + b.len <= a.stride;
+}
+
+// Outputs overlap nothing, except that token rows may be written exactly over
+// token rows that come in: every element is read by the thread that then
+// writes it.
+spade_status check_overlap(const Regions& rs) {
+  for (int i = 0; i < rs.n; ++i) {
+    if (!rs.r[i].out) continue;
+    for (int j = 0; j < rs.n; ++j) {
+      const Region &a = rs.r[i], &b = rs.r[j];
+      if (i == j || (b.out && j < i)) continue;
+      const bool same = a.row && b.row && !b.out && a.p == b.p && a.rows == b.rows && a.len == b.len &&
+                        (a.stride == b.stride || a.rows == 1);
+      if (!same && !disjoint(a, b)) return fail(SPADE_ERR_INVALID, "%s overlaps %s", a.name, b.name);
+    }
+  }
+  return SPADE_OK;
+}
+
+bool row_dtype(int dt) { return dt == SPADE_F32 || dt == SPADE_BF16; }
+int dtype_size(int dt) { return dt == SPADE_BF16 ? 2 : 4; }
+
+// A stride (0: packed) of rows of len elements, in elements.
+spade_status check_stride(const char* name, int64_t stride, long long len, long long* out) {
+  *out = stride == 0 ? len : stride;
+  if (*out < len || *out > (1LL << 40))
+    return fail(SPADE_ERR_INVALID, "%s: stride %lld for rows of %lld", name, (long long)stride, len);
+  return SPADE_OK;
+}
+
+spade_status check_operand(const char* name, const void* p, int dt) {
+  if (!p) return fail(SPADE_ERR_INVALID, "%s is null", name);
+  if (reinterpret_cast<uintptr_t>(p) % dtype_size(dt)) return fail(SPADE_ERR_INVALID, "%s is not aligned to its type", name);
+  return SPADE_OK;
+}
+
+spade_status check_scratch(const void* workspace, size_t ws_bytes, size_t need) {
+  if (!need) return SPADE_OK;
+  if (!workspace || ws_bytes < need)
+    return fail(SPADE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? ws_bytes : 0, need);
+  if (!aligned16(workspace)) return fail(SPADE_ERR_INVALID, "workspace must be 16-byte aligned");
+  return SPADE_OK;
+}
+
+// Sizes, types, strides and rotation of a Q/K pass; rope == nullptr skips the
+// rotation and the grid (workspace query).
+spade_status plan_qk(const spade_qk_desc* D, const spade_rope* rope, const int32_t* positions, QkArgs& a) {
+  memset(&a, 0, sizeof(a));
+  if (!D) return fail(SPADE_ERR_INVALID, "null descriptor");
+  const spade_qk_desc& d = *D;
+  if (d.rows < 0 || d.rows > kMaxRows || d.text_tokens < 0 || d.text_tokens > d.rows)
+    return fail(SPADE_ERR_INVALID, "rows=%lld, text_tokens=%lld", (long long)d.rows, (long long)d.text_tokens);
+  if (d.q_heads < 0 || d.k_heads < 0 || (!d.q_heads && !d.k_heads))
+    return fail(SPADE_ERR_INVALID, "q_heads=%d, k_heads=%d", d.q_heads, d.k_heads);
+  if (d.q_heads > SPADE_MAX_HEADS || d.k_heads > SPADE_MAX_HEADS)
+    return fail(SPADE_ERR_UNSUPPORTED, "q_heads=%d, k_heads=%d (up to %d)", d.q_heads, d.k_heads, SPADE_MAX_HEADS);
+  if (d.d < 2 || d.d > 2 * SPADE_ROPE_MAX_PAIRS || d.d % 2)
+    return fail(SPADE_ERR_UNSUPPORTED, "d=%d (even, 2..%d)", d.d, 2 * SPADE_ROPE_MAX_PAIRS);
+  if (!row_dtype(d.dt) || !row_dtype(d.weight_dt))
+    return fail(SPADE_ERR_INVALID, "unknown dtype %d, %d", d.dt, d.weight_dt);
+  if (d.norm < SPADE_QK_NORM_NONE || d.norm > SPADE_QK_NORM_HEAD) return fail(SPADE_ERR_INVALID, "norm %d", d.norm);
+  if (d.norm != SPADE_QK_NORM_NONE && !(d.eps >= 0.f && std::isfinite(d.eps)))
+    return fail(SPADE_ERR_INVALID, "eps %g", (double)d.eps);
+  a.rows = d.rows;
+  a.video_rows = d.rows - d.text_tokens;
+  a.heads[0] = d.q_heads;
+  a.heads[1] = d.k_heads;
+  a.d = d.d;
+  a.norm = d.norm;
+  a.eps = d.eps;
+  a.weight_bf16 = d.weight_dt == SPADE_BF16;
+  for (a.lanes = 1; a.lanes * 16 < d.d;) a.lanes *= 2;
+  spade_status st;
+  const int64_t strides[6] = {d.q_stride, d.k_stride, d.q_out_stride, d.k_out_stride, d.q_dout_stride, d.k_dout_stride};
+  long long* to[6] = {&a.x_stride[0], &a.x_stride[1], &a.out_stride[0], &a.out_stride[1], &a.dout_stride[0],
+                      &a.dout_stride[1]};
+  const char* names[6] = {"q", "k", "q output", "k output", "q gradient", "k gradient"};
+  for (int i = 0; i < 6; ++i)
+    if (a.heads[i & 1] && (st = check_stride(names[i], strides[i], (long long)a.heads[i & 1] * d.d, to[i])) != SPADE_OK)
+      return st;
+  if (!rope) return SPADE_OK;
+  if (rope->style != SPADE_ROPE_INTERLEAVED && rope->style != SPADE_ROPE_HALF)
+    return fail(SPADE_ERR_INVALID, "rotation style %d", rope->style);
+  if (rope->pairs < 0 || rope->pairs > d.d / 2)
+    return fail(SPADE_ERR_INVALID, "%d rotated pairs in heads of %d channels", rope->pairs, d.d);
+  if (rope->style == SPADE_ROPE_HALF && rope->pairs != d.d / 2)
+    return fail(SPADE_ERR_UNSUPPORTED, "half style with %d of %d pairs", rope->pairs, d.d / 2);
+  a.half = rope->style == SPADE_ROPE_HALF;
+  a.pairs = rope->pairs;
+  for (int i = 0; i < rope->pairs; ++i) {
+    if (rope->axis[i] < 0 || rope->axis[i] > 2) return fail(SPADE_ERR_INVALID, "pair %d: axis %d", i, rope->axis[i]);
+    if (!std::isfinite(rope->freq[i])) return fail(SPADE_ERR_INVALID, "pair %d: frequency not finite", i);
+    a.axis[i] = (uint8_t)rope->axis[i];
+    a.turn[i] = rope->freq[i] / 6.283185307179586476925286766559;
+  }
+  a.H = a.W = 1;
+  if (positions) {
+    if (d.text_tokens) return fail(SPADE_ERR_INVALID, "text_tokens with positions");
+    if (reinterpret_cast<uintptr_t>(positions) % 4) return fail(SPADE_ERR_INVALID, "positions are not aligned to their type");
+    a.positions = positions;
+  } else if (a.video_rows > 0) {
+    if (d.T <= 0 || d.H <= 0 || d.W <= 0) return fail(SPADE_ERR_INVALID, "grid has a non-positive extent");
+    const long long plane = (long long)d.H * d.W;
+    if (plane > INT32_MAX || plane * d.T > INT32_MAX) return fail(SPADE_ERR_UNSUPPORTED, "grid of 2^31 tokens or more");
+    if (d.token_offset < 0 || d.token_offset > plane * d.T || a.video_rows > plane * d.T - d.token_offset)
+      return fail(SPADE_ERR_INVALID, "rows past the end of the grid: offset %lld, %lld rows, %lld tokens",
+                  (long long)d.token_offset, a.video_rows, plane * d.T);
+    a.tok0 = (int)d.token_offset;
+    a.H = d.H;
+    a.W = d.W;
+  }
+  return SPADE_OK;
+}
+
+long long qk_weight_len(const QkArgs& a, int t) {
+  return a.norm == SPADE_QK_NORM_TOKEN ? (long long)a.heads[t] * a.d : (a.heads[t] ? a.d : 0);
+}
+
+// Pointers of a Q/K pass, and whether it can move 16 bytes at a time.
+spade_status bind_qk(const spade_qk_desc* D, QkArgs& a, const void* const x[2], const void* const dout[2],
+                     const void* const w[2], void* const out[2], float* const dw[2], const void* workspace,
+                     size_t ws_need) {
+  const char* xn[2] = {"q", "k"};
+  const char* gn[2] = {"dq_out", "dk_out"};
+  const char* on[2] = {dout ? "dq" : "q_out", dout ? "dk" : "k_out"};
+  const char* wn[2] = {"q_weight", "k_weight"};
+  const bool need_x = !dout || a.norm != SPADE_QK_NORM_NONE;
+  const int es = dtype_size(D->dt), ws = dtype_size(D->weight_dt);
+  Regions rs;
+  spade_status st;
+  a.vec = a.d % 16 == 0;
+  auto vec16 = [&](const void* p, long long stride_bytes) {
+    a.vec = a.vec && aligned16(p) && stride_bytes % 16 == 0;
+  };
+  for (int t = 0; t < 2; ++t) {
+    if (!a.heads[t]) {
+      if (dw && dw[t]) return fail(SPADE_ERR_INVALID, "weight gradient of an absent tensor");
+      continue;
+    }
+    const long long len = (long long)a.heads[t] * a.d;
+    if (a.rows) {
+      if (need_x && (st = check_operand(xn[t], x[t], D->dt)) != SPADE_OK) return st;
+      if (dout && (st = check_operand(gn[t], dout[t], D->dt)) != SPADE_OK) return st;
+      if ((st = check_operand(on[t], out[t], D->dt)) != SPADE_OK) return st;
+    }
+    if (w[t] && a.norm == SPADE_QK_NORM_NONE) return fail(SPADE_ERR_INVALID, "%s without a norm", wn[t]);
+    if (w[t] && (st = check_operand(wn[t], w[t], D->weight_dt)) != SPADE_OK) return st;
+    if (dw && dw[t] && (st = check_operand("weight gradient", dw[t], SPADE_F32)) != SPADE_OK) return st;
+    a.x[t] = need_x ? x[t] : nullptr;
+    a.dout[t] = dout ? dout[t] : nullptr;
+    a.out[t] = out[t];
+    a.weight[t] = w[t];
+    a.dweight[t] = dw ? dw[t] : nullptr;
+    if (a.x[t]) vec16(a.x[t], a.x_stride[t] * es);
+    if (a.dout[t]) vec16(a.dout[t], a.dout_stride[t] * es);
+    vec16(a.out[t], a.out_stride[t] * es);
+    if (w[t]) vec16(w[t], 0);
+    rs.add(xn[t], a.x[t], a.rows, a.x_stride[t] * es, len * es, false, true);
+    rs.add(gn[t], a.dout[t], a.rows, a.dout_stride[t] * es, len * es, false, true);
+    rs.add(on[t], a.out[t], a.rows, a.out_stride[t] * es, len * es, true, true);
+    rs.add(wn[t], w[t], 1, 0, qk_weight_len(a, t) * ws, false);
+    rs.add("weight gradient", a.dweight[t], 1, 0, qk_weight_len(a, t) * 4, true);
+  }
+  rs.add("positions", a.positions, 1, 0, a.rows * 12, false);
+  rs.add("workspace", workspace, 1, 0, (long long)ws_need, true);
+  // Q's output over K's input (or the reverse) is no in-place call: their heads are on other threads
+  for (int i = 0; i < rs.n; ++i)
+    for (int j = 0; j < rs.n; ++j)
+      if (rs.r[i].out && rs.r[i].name == on[0] && (rs.r[j].name == xn[1] || rs.r[j].name == gn[1]) &&
+          !disjoint(rs.r[i], rs.r[j]))
+        return fail(SPADE_ERR_INVALID, "%s overlaps %s", rs.r[i].name, rs.r[j].name);
+      else if (rs.r[i].out && rs.r[i].name == on[1] && (rs.r[j].name == xn[0] || rs.r[j].name == gn[0]) &&
+               !disjoint(rs.r[i], rs.r[j]))
+        return fail(SPADE_ERR_INVALID, "%s overlaps %s", rs.r[i].name, rs.r[j].name);
+  return check_overlap(rs);
+}
+
+// Sizes, types, strides and parameters of a row pass; bwd: the gradients'
+// strides are checked too.
+spade_status plan_row(const spade_row_desc* D, const spade_row_params* P, bool bwd, RowArgs& a) {
+  memset(&a, 0, sizeof(a));
+  if (!D) return fail(SPADE_ERR_INVALID, "null descriptor");
+  const spade_row_desc& d = *D;
+  if (d.rows < 0 || d.rows > kMaxRows || d.groups < 1 || d.groups > kMaxRows || d.rows % d.groups)
+    return fail(SPADE_ERR_INVALID, "rows=%lld in groups=%lld", (long long)d.rows, (long long)d.groups);
+  if (d.dim < 1) return fail(SPADE_ERR_INVALID, "dim=%d", d.dim);
+  if (d.dim > SPADE_ROW_MAX_DIM) return fail(SPADE_ERR_UNSUPPORTED, "dim=%d (up to %d)", d.dim, SPADE_ROW_MAX_DIM);
+  if (!row_dtype(d.x_dt) || !row_dtype(d.branch_dt) || !row_dtype(d.param_dt))
+    return fail(SPADE_ERR_INVALID, "unknown dtype %d, %d, %d", d.x_dt, d.branch_dt, d.param_dt);
+  if (d.x_dt == SPADE_BF16 && d.branch_dt == SPADE_F32)
+    return fail(SPADE_ERR_UNSUPPORTED, "a float32 branch on a bfloat16 stream");
+  if (d.norm < SPADE_NORM_NONE || d.norm > SPADE_NORM_LAYER || d.post_norm < SPADE_NORM_NONE ||
+      d.post_norm > SPADE_NORM_LAYER)
+    return fail(SPADE_ERR_INVALID, "norm %d, post_norm %d", d.norm, d.post_norm);
+  a.rows = d.rows;
+  a.groups = d.groups;
+  a.rows_per_group = d.rows / d.groups;
+  a.chunks = 1;
+  a.dim = d.dim;
+  a.norm = d.norm;
+  a.post_norm = d.post_norm;
+  a.eps = d.eps;
+  a.post_eps = d.post_eps;
+  a.residual_scale = d.residual_scale;
+  a.x_bf16 = d.x_dt == SPADE_BF16;
+  a.branch_bf16 = d.branch_dt == SPADE_BF16;
+  a.param_bf16 = d.param_dt == SPADE_BF16;
+  const struct { const char* name; int64_t stride; long long* to; bool used; } strides[] = {
+      {"x", d.x_stride, &a.x_stride, true},
+      {"y", d.y_stride, &a.y_stride, true},
+      {"x_out", d.x_out_stride, &a.x_out_stride, !bwd},
+      {"h", d.h_stride, &a.h_stride, !bwd},
+      {"dx_out", d.dx_out_stride, &a.dx_out_stride, bwd},
+      {"dh", d.dh_stride, &a.dh_stride, bwd},
+      {"dx", d.dx_stride, &a.dx_stride, bwd},
+      {"dy", d.dy_stride, &a.dy_stride, bwd},
+      {"gate", d.gate_stride, &a.gate_stride, true},
+      {"scale", d.scale_stride, &a.scale_stride, true},
+      {"shift", d.shift_stride, &a.shift_stride, true}};
+  spade_status st;
+  for (const auto& s : strides)
+    if (s.used && (st = check_stride(s.name, s.stride, d.dim, s.to)) != SPADE_OK) return st;
+  if (P) {
+    const struct { const char* name; const void* p; const void** to; } params[] = {
+        {"gate", P->gate, &a.gate},       {"post_weight", P->post_weight, &a.post_weight},
+        {"weight", P->weight, &a.weight}, {"bias", P->bias, &a.bias},
+        {"scale", P->scale, &a.scale},    {"shift", P->shift, &a.shift}};
+    for (const auto& p : params) {
+      if (p.p && (st = check_operand(p.name, p.p, d.param_dt)) != SPADE_OK) return st;
+      *p.to = p.p;
+    }
+  }
+  return SPADE_OK;
+}
+
+spade_status check_eps(int norm, float eps) {
+  if (norm != SPADE_NORM_NONE && !(eps >= 0.f && std::isfinite(eps)))
+    return fail(SPADE_ERR_INVALID, "eps %g", (double)eps);
+  return SPADE_OK;
+}
+
+// What the residual half and the norm half of a pass need and may not have.
+spade_status check_halves(RowArgs& a, bool res, bool norm) {
+  spade_status st;
+  if (norm) {
+    if (a.norm == SPADE_NORM_NONE) return fail(SPADE_ERR_INVALID, "norm is none");
+    if ((st = check_eps(a.norm, a.eps)) != SPADE_OK) return st;
+  } else {
+    if (a.weight || a.bias || a.scale || a.shift) return fail(SPADE_ERR_INVALID, "norm parameters without a norm");
+    a.norm = SPADE_NORM_NONE;
+  }
+  if (res) {
+    if (a.post_weight && a.post_norm == SPADE_NORM_NONE)
+      return fail(SPADE_ERR_INVALID, "post_weight without a post_norm");
+    if ((st = check_eps(a.post_norm, a.post_eps)) != SPADE_OK) return st;
+  } else {
+    if (a.gate || a.post_weight) return fail(SPADE_ERR_INVALID, "gate parameters without a residual");
+    a.post_norm = SPADE_NORM_NONE;
+  }
+  return SPADE_OK;
+}
+
+void add_params(Regions& rs, const RowArgs& a) {
+  const int ep = a.param_bf16 ? 2 : 4;
+  const long long len = (long long)a.dim * ep;
+  rs.add("gate", a.gate, a.groups, a.gate_stride * ep, len, false);
+  rs.add("scale", a.scale, a.groups, a.scale_stride * ep, len, false);
+  rs.add("shift", a.shift, a.groups, a.shift_stride * ep, len, false);
+  rs.add("post_weight", a.post_weight, 1, 0, len, false);
+  rs.add("weight", a.weight, 1, 0, len, false);
+  rs.add("bias", a.bias, 1, 0, len, false);
+}
+
+struct RowOperand {
+  const char* name;
+  const void* p;
+  long long stride;
+  bool branch, out, optional;
+};
+
+// Row operands: present, aligned, apart from one another.
+spade_status check_rows(const RowArgs& a, const RowOperand* ops, int n, Regions& rs) {
+  spade_status st;
+  for (int i = 0; i < n; ++i) {
+    const int dt = (ops[i].branch ? a.branch_bf16 : a.x_bf16) ? SPADE_BF16 : SPADE_F32;
+    if (!ops[i].p && (ops[i].optional || !a.rows)) continue;
+    if ((st = check_operand(ops[i].name, ops[i].p, dt)) != SPADE_OK) return st;
+    const int es = dtype_size(dt);
+    rs.add(ops[i].name, ops[i].p, a.rows, ops[i].stride * es, (long long)a.dim * es, ops[i].out, true);
+  }
+  return check_overlap(rs);
+}
+
+spade_status run_row_fwd(const spade_row_desc* desc, const spade_row_params* params, const void* x, const void* y,
+                         void* x_out, void* h, bool res, bool norm, cudaStream_t s, const char* where) {
+  RowArgs a;
+  spade_status st = plan_row(desc, params, false, a);
+  if (st != SPADE_OK) return st;
+  if ((st = check_halves(a, res, norm)) != SPADE_OK) return st;
+  a.x = x;
+  a.y = y;
+  a.x_out = x_out;
+  a.h = h;
+  const RowOperand ops[] = {{"x", x, a.x_stride, false, false, false},
+                            {"y", y, a.y_stride, true, false, !res},
+                            {"x_out", x_out, a.x_out_stride, false, true, !res},
+                            {"h", h, a.h_stride, true, true, !norm}};
+  Regions rs;
+  add_params(rs, a);
+  if ((st = check_rows(a, ops, 4, rs)) != SPADE_OK) return st;
+  if (!a.rows) return SPADE_OK;
+  const cudaError_t e = launch_row_fwd(a, s);
+  return e == cudaSuccess ? SPADE_OK : cuda_fail(e, where);
+}
+
+spade_status run_row_bwd(const spade_row_desc* desc, const spade_row_params* params, const void* dx_out,
+                         const void* dh, const void* x, const void* y, void* dx, void* dy,
+                         const spade_row_grads* grads, void* workspace, size_t ws_bytes, bool res, bool norm,
+                         cudaStream_t s, const char* where) {
+  RowArgs a;
+  spade_status st = plan_row(desc, params, true, a);
+  if (st != SPADE_OK) return st;
+  if ((st = check_halves(a, res, norm)) != SPADE_OK) return st;
+  a.x = x;
+  a.y = y;
+  a.dx_out = dx_out;
+  a.dh = dh;
+  a.dx = dx;
+  a.dy = dy;
+  if (grads) {
+    a.dgate = grads->gate;
+    a.dpost_weight = grads->post_weight;
+    a.dweight = grads->weight;
+    a.dbias = grads->bias;
+    a.dscale = grads->scale;
+    a.dshift = grads->shift;
+  }
+  if (!norm && (a.dweight || a.dbias || a.dscale || a.dshift))
+    return fail(SPADE_ERR_INVALID, "gradients of norm parameters without a norm");
+  if (!res && (a.dgate || a.dpost_weight)) return fail(SPADE_ERR_INVALID, "gradients of gate parameters without a residual");
+  if (a.dpost_weight && a.post_norm == SPADE_NORM_NONE)
+    return fail(SPADE_ERR_INVALID, "gradient of post_weight without a post_norm");
+  Regions rs;
+  add_params(rs, a);
+  const struct { const char* name; float* p; long long len; } gs[] = {
+      {"gate gradient", a.dgate, a.groups * a.dim},   {"post_weight gradient", a.dpost_weight, a.dim},
+      {"weight gradient", a.dweight, a.dim},          {"bias gradient", a.dbias, a.dim},
+      {"scale gradient", a.dscale, a.groups * a.dim}, {"shift gradient", a.dshift, a.groups * a.dim}};
+  for (const auto& g : gs) {
+    if (g.p && (st = check_operand(g.name, g.p, SPADE_F32)) != SPADE_OK) return st;
+    rs.add(g.name, g.p, 1, 0, g.len * 4, true);
+  }
+  const RowOperand ops[] = {{"x", x, a.x_stride, false, false, !norm},
+                            {"y", y, a.y_stride, true, false, !res},
+                            {norm && !res ? "dres" : "dx_out", dx_out, a.dx_out_stride, false, false, norm},
+                            {"dh", dh, a.dh_stride, true, false, !norm},
+                            {"dx", dx, a.dx_stride, false, true, !norm},
+                            {"dy", dy, a.dy_stride, true, true, !res}};
+  if (!a.rows) {
+    if ((st = check_rows(a, ops, 6, rs)) != SPADE_OK) return st;
+    for (const auto& g : gs)
+      if (g.p) {
+        const cudaError_t e = cudaMemsetAsync(g.p, 0, sizeof(float) * (size_t)g.len, s);
+        if (e != cudaSuccess) return cuda_fail(e, where);
+      }
+    return SPADE_OK;
+  }
+  const bool weights = a.dweight || a.dbias || a.dpost_weight;
+  const RowPlan plan = plan_row_bwd(a.rows, a.groups, a.dim, weights);
+  a.chunks = plan.chunks;
+  if ((st = check_scratch(workspace, ws_bytes, plan.floats * sizeof(float))) != SPADE_OK) return st;
+  a.part = plan.floats ? static_cast<float*>(workspace) : nullptr;
+  rs.add("workspace", a.part, 1, 0, (long long)(plan.floats * sizeof(float)), true);
+  if ((st = check_rows(a, ops, 6, rs)) != SPADE_OK) return st;
+  const cudaError_t e = launch_row_bwd(a, plan.grid, s);
+  return e == cudaSuccess ? SPADE_OK : cuda_fail(e, where);
 }
 
 }  // namespace
@@ -859,6 +1268,134 @@ spade_status spade_grouped_attn_host(const void* q_host, const void* k_host, con
   }
   e = cudaGetLastError();
   return e == cudaSuccess ? SPADE_OK : cuda_fail(e, "host-to-host layer");
+}
+
+// ---- row passes around the attention ----
+
+spade_status spade_rope_axes(spade_rope* rope, const int32_t pairs[3], const double theta[3], const double scale[3],
+                             spade_rope_style style, int shared_ladder) {
+  if (!rope || !pairs || !theta || !scale) return fail(SPADE_ERR_INVALID, "null pointer");
+  if (style != SPADE_ROPE_INTERLEAVED && style != SPADE_ROPE_HALF)
+    return fail(SPADE_ERR_INVALID, "rotation style %d", (int)style);
+  long long total = 0;
+  for (int a = 0; a < 3; ++a) {
+    if (pairs[a] < 0) return fail(SPADE_ERR_INVALID, "axis %d: %d pairs", a, pairs[a]);
+    if (!(theta[a] > 0.0) || !std::isfinite(theta[a]) || !std::isfinite(scale[a]))
+      return fail(SPADE_ERR_INVALID, "axis %d: theta %g, scale %g", a, theta[a], scale[a]);
+    total += pairs[a];
+  }
+  if (total > SPADE_ROPE_MAX_PAIRS)
+    return fail(SPADE_ERR_UNSUPPORTED, "%lld rotated pairs (up to %d)", total, SPADE_ROPE_MAX_PAIRS);
+  spade_rope r;
+  memset(&r, 0, sizeof(r));
+  r.style = style;
+  for (int a = 0; a < 3; ++a)
+    for (int i = 0; i < pairs[a]; ++i) {
+      const double base = shared_ladder ? theta[0] : theta[a];
+      const double at = shared_ladder ? (double)r.pairs / (double)total : (double)i / (double)pairs[a];
+      r.axis[r.pairs] = a;
+      r.freq[r.pairs] = scale[a] * pow(base, -at);
+      ++r.pairs;
+    }
+  *rope = r;
+  return SPADE_OK;
+}
+
+size_t spade_qk_norm_rope_bwd_workspace_bytes(const spade_qk_desc* desc) {
+  QkArgs a;
+  if (plan_qk(desc, nullptr, nullptr, a) != SPADE_OK) return 0;
+  return a.rows ? qk_bwd_floats(a) * sizeof(float) : 0;
+}
+
+spade_status spade_qk_norm_rope(const spade_qk_desc* desc, const spade_rope* rope, const int32_t* positions,
+                                const void* q, const void* k, const void* q_weight, const void* k_weight, void* q_out,
+                                void* k_out, spade_stream_t stream) {
+  if (!rope) return fail(SPADE_ERR_INVALID, "null rotation");
+  QkArgs a;
+  spade_status st = plan_qk(desc, rope, positions, a);
+  if (st != SPADE_OK) return st;
+  const void* x[2] = {q, k};
+  void* out[2] = {q_out, k_out};
+  const void* w[2] = {q_weight, k_weight};
+  if ((st = bind_qk(desc, a, x, nullptr, w, out, nullptr, nullptr, 0)) != SPADE_OK) return st;
+  if (!a.rows) return SPADE_OK;
+  const cudaError_t e = launch_qk_fwd(a, desc->dt == SPADE_BF16, as_cuda(stream));
+  return e == cudaSuccess ? SPADE_OK : cuda_fail(e, "qk_norm_rope");
+}
+
+spade_status spade_qk_norm_rope_bwd(const spade_qk_desc* desc, const spade_rope* rope, const int32_t* positions,
+                                    const void* dq_out, const void* dk_out, const void* q, const void* k,
+                                    const void* q_weight, const void* k_weight, void* dq, void* dk, float* dq_weight,
+                                    float* dk_weight, void* workspace, size_t ws_bytes, spade_stream_t stream) {
+  if (!rope) return fail(SPADE_ERR_INVALID, "null rotation");
+  QkArgs a;
+  spade_status st = plan_qk(desc, rope, positions, a);
+  if (st != SPADE_OK) return st;
+  const bool normed = a.norm != SPADE_QK_NORM_NONE;
+  const void* x[2] = {normed ? q : nullptr, normed ? k : nullptr};
+  const void* dout[2] = {dq_out, dk_out};
+  void* out[2] = {dq, dk};
+  const void* w[2] = {q_weight, k_weight};
+  float* dw[2] = {dq_weight, dk_weight};
+  if (!normed && (dq_weight || dk_weight)) return fail(SPADE_ERR_INVALID, "weight gradient without a norm");
+  const size_t need = (dq_weight || dk_weight) && a.rows ? qk_bwd_floats(a) * sizeof(float) : 0;
+  if ((st = check_scratch(workspace, ws_bytes, need)) != SPADE_OK) return st;
+  if ((st = bind_qk(desc, a, x, dout, w, out, dw, workspace, need)) != SPADE_OK) return st;
+  const cudaStream_t s = as_cuda(stream);
+  if (!a.rows) {
+    for (int t = 0; t < 2; ++t)
+      if (dw[t]) {
+        const cudaError_t e = cudaMemsetAsync(dw[t], 0, sizeof(float) * qk_weight_len(a, t), s);
+        if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope_bwd");
+      }
+    return SPADE_OK;
+  }
+  if (need) a.part = static_cast<float*>(workspace);
+  const cudaError_t e = launch_qk_bwd(a, desc->dt == SPADE_BF16, s);
+  return e == cudaSuccess ? SPADE_OK : cuda_fail(e, "qk_norm_rope_bwd");
+}
+
+spade_status spade_norm_modulate(const spade_row_desc* desc, const spade_row_params* params, const void* x, void* h,
+                                 spade_stream_t stream) {
+  return run_row_fwd(desc, params, x, nullptr, nullptr, h, false, true, as_cuda(stream), "norm_modulate");
+}
+
+spade_status spade_gate_residual(const spade_row_desc* desc, const spade_row_params* params, const void* x,
+                                 const void* y, void* x_out, spade_stream_t stream) {
+  return run_row_fwd(desc, params, x, y, x_out, nullptr, true, false, as_cuda(stream), "gate_residual");
+}
+
+spade_status spade_gate_residual_norm(const spade_row_desc* desc, const spade_row_params* params, const void* x,
+                                      const void* y, void* x_out, void* h, spade_stream_t stream) {
+  return run_row_fwd(desc, params, x, y, x_out, h, true, true, as_cuda(stream), "gate_residual_norm");
+}
+
+size_t spade_row_bwd_workspace_bytes(const spade_row_desc* desc) {
+  RowArgs a;
+  if (plan_row(desc, nullptr, true, a) != SPADE_OK || !a.rows) return 0;
+  return plan_row_bwd(a.rows, a.groups, a.dim, true).floats * sizeof(float);
+}
+
+spade_status spade_norm_modulate_bwd(const spade_row_desc* desc, const spade_row_params* params, const void* dh,
+                                     const void* dres, const void* x, void* dx, const spade_row_grads* grads,
+                                     void* workspace, size_t ws_bytes, spade_stream_t stream) {
+  return run_row_bwd(desc, params, dres, dh, x, nullptr, dx, nullptr, grads, workspace, ws_bytes, false, true,
+                     as_cuda(stream), "norm_modulate_bwd");
+}
+
+spade_status spade_gate_residual_bwd(const spade_row_desc* desc, const spade_row_params* params, const void* dx_out,
+                                     const void* y, void* dy, const spade_row_grads* grads, void* workspace,
+                                     size_t ws_bytes, spade_stream_t stream) {
+  return run_row_bwd(desc, params, dx_out, nullptr, nullptr, y, nullptr, dy, grads, workspace, ws_bytes, true, false,
+                     as_cuda(stream), "gate_residual_bwd");
+}
+
+spade_status spade_gate_residual_norm_bwd(const spade_row_desc* desc, const spade_row_params* params,
+                                          const void* dx_out, const void* dh, const void* x, const void* y, void* dx,
+                                          void* dy, const spade_row_grads* grads, void* workspace, size_t ws_bytes,
+                                          spade_stream_t stream) {
+  return run_row_bwd(desc, params, dx_out, dh, x, y, dx, dy, grads, workspace, ws_bytes, true, true, as_cuda(stream),
+                     "gate_residual_norm_bwd");
 }
 
 spade_status spade_last_device_status(spade_stream_t stream) {

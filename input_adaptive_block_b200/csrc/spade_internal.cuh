@@ -9,6 +9,7 @@
 
 #define SPADE_MAX_SCHEMES 4
 #define SPADE_MAX_HEADS 128
+#define SPADE_ROW_MAX_DIM 16384
 #define SPADE_SELECT_MAX_NB 1024
 #define SPADE_SELECT_MAX_HEADS 1024
 #define SPADE_ESTIMATE_MAX_NB 2048
@@ -103,6 +104,57 @@ cudaError_t launch_bounded_wait_selftest(int* status, long long timeout_ns, cuda
 size_t sics_workspace_floats(const Geo* cand, int n_cand, int heads);
 cudaError_t launch_sics(const void* q, const void* k, const Geo* cand, int n_cand, int heads, int d, spade_dtype dt,
                         float* ws, float* scores, int* choice, cudaStream_t s);
+
+// One row pass of the residual stream (k_row_norm.cu).  Null pointers: no
+// such operand (parameters: the identity); strides in elements.
+struct RowArgs {
+  long long rows, groups, rows_per_group, chunks;
+  int dim, norm, post_norm;
+  float eps, post_eps, residual_scale;
+  bool x_bf16, branch_bf16, param_bf16;
+  const void *x, *y;                                  // forward inputs (x also backward)
+  void *x_out, *h;                                    // forward outputs
+  const void *dx_out, *dh;                            // gradients coming in
+  void *dx, *dy;                                      // gradients going out
+  const void *gate, *post_weight, *weight, *bias, *scale, *shift;
+  float *dgate, *dpost_weight, *dweight, *dbias, *dscale, *dshift;
+  long long x_stride, y_stride, x_out_stride, h_stride, dx_out_stride, dh_stride, dx_stride, dy_stride;
+  long long gate_stride, scale_stride, shift_stride;
+  float* part;                                        // column sums of the backward units
+};
+struct RowPlan {
+  long long chunks;     // units a modulation group is cut into
+  int grid;
+  size_t floats;        // workspace
+};
+RowPlan plan_row_bwd(long long rows, long long groups, int dim, bool weights);
+cudaError_t launch_row_fwd(const RowArgs& a, cudaStream_t s);
+cudaError_t launch_row_bwd(const RowArgs& a, int grid, cudaStream_t s);
+
+// Norm and rotation of Q and K (k_qk_rope.cu).  Index 0 is Q, 1 is K; a
+// tensor without heads is absent.
+struct QkArgs {
+  long long rows, video_rows;
+  int tok0, H, W;                  // grid position of row 0 (no positions given)
+  int heads[2], d, lanes;          // lanes: threads per head, a power of two
+  int norm;
+  float eps;
+  bool weight_bf16, half, vec;
+  const void* x[2];                // raw rows
+  const void* dout[2];             // backward: gradient coming in
+  void* out[2];                    // forward: result; backward: gradient going out
+  const void* weight[2];
+  float* dweight[2];
+  long long x_stride[2], dout_stride[2], out_stride[2];
+  const int* positions;            // [rows, 3] or null
+  float* part;
+  int pairs;
+  uint8_t axis[SPADE_ROPE_MAX_PAIRS];
+  double turn[SPADE_ROPE_MAX_PAIRS];   // turns per unit of position
+};
+size_t qk_bwd_floats(const QkArgs& a);
+cudaError_t launch_qk_fwd(const QkArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_qk_bwd(const QkArgs& a, bool bf16, cudaStream_t s);
 
 int num_sms();                               // SM count of the current device
 long long device_wait_timeout_ns();          // limit for every bounded device wait
