@@ -23,7 +23,8 @@ BUILD = os.path.join(ROOT, "_build", "spade")
 LIB = os.path.join(PKG, "libspade.so")
 
 SOURCES = ["spade_api.cu", "k_tile_summarize.cu", "k_estimate.cu", "k_estimate_tc.cu", "k_select.cu", "k_sics.cu",
-           "k_qk_rope.cu", "k_row_norm.cu", "k_attn_simt.cu", "k_attn_tc.cu"]
+           "k_qk_rope.cu", "k_row.cu", "k_row_bf16.cu", "k_row_mixed.cu",
+           "k_row_f32.cu", "k_attn_simt.cu", "k_attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -5,19 +5,23 @@
 // turns, position times turns-per-unit in float64, its nearest integer is
 // taken off there and the rest (at most half a turn, rounded once to float32)
 // goes to sincospif: positions anywhere in int32 keep an angle good to
-// float32.  A token's angles are computed once and serve every head of Q and
-// of K.
+// float32.  A token's angles are computed once, ahead of its data, and serve
+// every head of Q and of K.
 //
 // Forward:  n = x * rstd * w (rms over the token's heads * d values, over
 //           each head's d, or no norm), out = rotation of n.
 // Backward: u = dout rotated back, dw = sum of u * x * rstd over the rows (and
 //           heads, for the per-head norm), dx = rstd (w u - x rstd^2 mean(w u x)).
 //
-// `lanes` threads share a head (d / 16 rounded up to a power of two), each
-// owning eight pairs: the same pairs of every head it meets, so their sines
-// and cosines stay in its registers for the whole token.  A block takes kTok
-// tokens at a time and loads all of them before it uses the first, which keeps
-// enough bytes in flight; their sums share one barrier.  Bound by memory.
+// `lanes` threads (d / 16 rounded up to a power of two) share a head, sixteen
+// channels each: a unit.  The units of Q and K are numbered through; a thread
+// has UPT of them, the same of every token, and the same eight pairs in each,
+// so weights and the sums of their gradient stay in its registers and a
+// token's sines and cosines are read once for all its units.  Channels are
+// owned in pieces of P that alternate between the lanes, so that a warp's
+// access is contiguous.  Tokens are copied ahead into a ring in shared memory,
+// by the thread that uses them (no barrier); a block takes K tokens at a time,
+// whose sums share one barrier.  Bound by memory.
 #include "row_io.cuh"
 #include "spade_internal.cuh"
 
@@ -26,392 +30,469 @@ namespace {
 
 using namespace rowio;
 
-constexpr int kTok = 2;     // tokens a block holds at once
+constexpr int kDepthMax = 14;
 
-// A thread's eight pairs of one head: first elements in a, second in b.
-template <typename T>
-struct Unit {
-  Raw8<T> lo, hi;
-};
-
-// Pairs of a thread: eight neighbours (VEC), or every lanes-th pair.
-template <bool VEC>
-__device__ __forceinline__ int pair_of(int j, int e, int lanes) {
-  return VEC ? j * 8 + e : e * lanes + j;
+// Channel of a thread's element e (0..15).  Interleaved: pairs (2m, 2m + 1)
+// are neighbours in a piece (P = 1: two single accesses).  Halves: elements
+// m and m + 8 are half a head apart.
+template <int P, bool HALF>
+__device__ __forceinline__ int channel(int j, int lanes, int e, int d) {
+  constexpr int O = !HALF && P == 1 ? 2 : P;
+  if (HALF) return ((e & 7) / O * lanes + j) * O + (e & 7) % O + (e >= 8 ? d >> 1 : 0);
+  return (e / O * lanes + j) * O + e % O;
 }
-
-// Element offset of pair p's first and second element in a head.
-__device__ __forceinline__ int first_of(int p, bool half) { return half ? p : 2 * p; }
-__device__ __forceinline__ int second_of(int p, bool half, int d) { return half ? p + (d >> 1) : 2 * p + 1; }
-
-// The sixteen elements in head order of a VEC unit: [8j, 8j+8) and d/2 later
-// (halves), or [16j, 16j+16) (neighbouring pairs).
-template <typename T>
-__device__ __forceinline__ void load_unit(Unit<T>& u, const T* head, int j, bool half, int d) {
-  const T* p = head + (half ? 8 * j : 16 * j);
-  load_raw(u.lo, p);
-  load_raw(u.hi, p + (half ? (d >> 1) : 8));
+template <int P, bool HALF>
+__device__ __forceinline__ bool owned(int j, int lanes, int e, int d) {
+  return HALF ? channel<P, HALF>(j, lanes, e & 7, d) < (d >> 1) : channel<P, HALF>(j, lanes, e, d) < d;
 }
-template <typename T>
-__device__ __forceinline__ void split_unit(float (&a)[8], float (&b)[8], const Unit<T>& u, bool half) {
-  float lo[8], hi[8];
-  unpack(lo, u.lo);
-  unpack(hi, u.hi);
+// Where the angle of pair p lies: as entry m of lane j, so that a thread reads
+// its eight as four 16-byte words, without bank conflicts.
+template <int P, bool HALF>
+__device__ __forceinline__ int angle_slot(int p, int lanes) {
+  constexpr int O = !HALF && P == 1 ? 2 : P;
+  const int c = HALF ? p : 2 * p, piece = c / O;
+  const int e = piece / lanes * O + c % O, j = piece & (lanes - 1), m = HALF ? e : e >> 1;
+  return ((m >> 1) * lanes + j) * 2 + (m & 1);
+}
+template <bool HALF>
+__device__ __forceinline__ constexpr int first_of(int m) { return HALF ? m : 2 * m; }
+template <bool HALF>
+__device__ __forceinline__ constexpr int second_of(int m) { return HALF ? m + 8 : 2 * m + 1; }
+
+// A thread's unit: its sixteen elements in global memory and in the ring.
+template <typename T, int P, bool HALF>
+__device__ __forceinline__ void load16(float (&v)[16], const T* head, bool in, int j, int lanes, int d) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    a[e] = half ? lo[e] : (e < 4 ? lo[2 * e] : hi[2 * e - 8]);
-    b[e] = half ? hi[e] : (e < 4 ? lo[2 * e + 1] : hi[2 * e - 7]);
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store_unit(T* head, const float (&a)[8], const float (&b)[8], int j, bool half, int d) {
-  float lo[8], hi[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int i = e >> 1;
-    lo[e] = half ? a[e] : (e & 1 ? b[i] : a[i]);
-    hi[e] = half ? b[e] : (e & 1 ? b[4 + i] : a[4 + i]);
-  }
-  T* p = head + (half ? 8 * j : 16 * j);
-  store_vec(p, lo);
-  store_vec(p + (half ? (d >> 1) : 8), hi);
-}
-
-// One thread's share of one head, as pair elements in float32; absent pairs
-// and heads are zero.
-template <bool VEC, typename T>
-struct Share {
-  Unit<T> u;                 // VEC
-  float a[VEC ? 1 : 8], b[VEC ? 1 : 8];
-
-  __device__ __forceinline__ void load(const T* head, bool in, int j, int lanes, bool half, int d) {
-    if (VEC) {
-      if (in) load_unit(u, head, j, half, d);
-      else {
-        clear_raw(u.lo);
-        clear_raw(u.hi);
-      }
+  for (int e = 0; e < 16; e += P) {
+    if (in && owned<P, HALF>(j, lanes, e, d)) {
+      load_piece<T, P>(v + e, head + channel<P, HALF>(j, lanes, e, d));
     } else {
 #pragma unroll
-      for (int e = 0; e < (VEC ? 1 : 8); ++e) {
-        const int p = pair_of<false>(j, e, lanes);
-        const bool ok = in && p < (d >> 1);
-        a[e] = ok ? to_float(head[first_of(p, half)]) : 0.f;
-        b[e] = ok ? to_float(head[second_of(p, half, d)]) : 0.f;
-      }
+      for (int q = 0; q < P; ++q) v[e + q] = 0.f;
     }
   }
-  __device__ __forceinline__ void get(float (&oa)[8], float (&ob)[8], bool half) const {
-    if (VEC) {
-      split_unit(oa, ob, u, half);
-    } else {
+}
+template <typename T, int P, bool HALF>
+__device__ __forceinline__ void store16(T* head, const float (&v)[16], int j, int lanes, int d) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        oa[e] = a[VEC ? 0 : e];
-        ob[e] = b[VEC ? 0 : e];
-      }
-    }
-  }
+  for (int e = 0; e < 16; e += P)
+    if (owned<P, HALF>(j, lanes, e, d)) store_piece<P>(head + channel<P, HALF>(j, lanes, e, d), v + e);
+}
+// The ring keeps a unit's pieces [16 / P][threads][P].
+template <typename T, int P, bool HALF>
+__device__ __forceinline__ void fetch16(uint32_t to, const T* head, int j, int lanes, int d) {
+#pragma unroll
+  for (int e = 0; e < 16; e += P)
+    if (owned<P, HALF>(j, lanes, e, d))
+      copy_async<P * (int)sizeof(T)>(to + (e / P * blockDim.x + threadIdx.x) * P * (int)sizeof(T),
+                                     head + channel<P, HALF>(j, lanes, e, d));
+}
+template <typename T, int P>
+__device__ __forceinline__ void ring16(float (&v)[16], const unsigned char* at) {
+  const T* p = reinterpret_cast<const T*>(at);
+#pragma unroll
+  for (int e = 0; e < 16; e += P) load_piece<T, P>(v + e, p + (e / P * blockDim.x + threadIdx.x) * P);
+}
+// What is not copied reads as zero.
+template <typename T, int P, bool HALF>
+__device__ __forceinline__ void clear16(unsigned char* at, bool in, int j, int lanes, int d) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (!in || !owned<P, HALF>(j, lanes, e, d))
+      reinterpret_cast<T*>(at)[(e / P * blockDim.x + threadIdx.x) * P + e % P] = T(0.f);
+}
+
+struct Turns {
+  double turn[SPADE_ROPE_MAX_PAIRS];
+  int axis[SPADE_ROPE_MAX_PAIRS];
 };
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_share(T* head, const float (&a)[8], const float (&b)[8], int j, int lanes,
-                                            bool half, int d) {
-  if (VEC) {
-    store_unit(head, a, b, j, half, d);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int p = pair_of<false>(j, e, lanes);
-      if (p < (d >> 1)) {
-        store_one(head + first_of(p, half), a[e]);
-        store_one(head + second_of(p, half, d), b[e]);
-      }
-    }
-  }
-}
-template <bool VEC>
-__device__ __forceinline__ void load_weight(float (&a)[8], float (&b)[8], const void* w, bool bf16, int off, bool in,
-                                            int j, int lanes, bool half, int d) {
-  if (!w || !in) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = b[e] = 1.f;
-  } else if (bf16) {
-    Share<VEC, __nv_bfloat16> s;
-    s.load(static_cast<const __nv_bfloat16*>(w) + off, true, j, lanes, half, d);
-    s.get(a, b, half);
-  } else {
-    Share<VEC, float> s;
-    s.load(static_cast<const float*>(w) + off, true, j, lanes, half, d);
-    s.get(a, b, half);
-  }
-}
 
 // Cosine and sine of every pair of the block's next tokens.
-__device__ __forceinline__ void angles(const QkArgs& a, long long r0, int n, float2* cs) {
+template <int P, bool HALF, int K>
+__device__ __forceinline__ void angles(const QkArgs& a, const Turns& tu, long long r0, long long r1, float2* cs) {
   const int half_d = a.d >> 1;
-  for (int i = threadIdx.x; i < n * half_d; i += blockDim.x) {
+  for (int i = threadIdx.x; i < K * half_d; i += blockDim.x) {
     const int k = i / half_d, p = i - k * half_d;
     const long long r = r0 + k;
     float2 v = make_float2(1.f, 0.f);
-    if (p < a.pairs && r < a.video_rows) {
+    if (p < a.pairs && r < a.video_rows && r < r1) {
+      const int axis = tu.axis[p];
       int pos;
       if (a.positions) {
-        pos = a.positions[r * 3 + a.axis[p]];
+        pos = a.positions[r * 3 + axis];
       } else {
-        const int tok = a.tok0 + (int)r;
-        const int row = tok / a.W;
-        pos = a.axis[p] == 2 ? tok - row * a.W : (a.axis[p] == 1 ? row % a.H : row / a.H);
+        const unsigned tok = (unsigned)a.tok0 + (unsigned)r, row = tok / (unsigned)a.W;
+        pos = axis == 2 ? tok - row * (unsigned)a.W
+                        : (axis == 1 ? row % (unsigned)a.H : row / (unsigned)a.H);
       }
-      const double t = (double)pos * a.turn[p];
+      const double t = (double)pos * tu.turn[p];
       sincospif(2.f * (float)(t - rint(t)), &v.y, &v.x);
     }
-    cs[i] = v;
+    cs[k * 8 * a.lanes + angle_slot<P, HALF>(p, a.lanes)] = v;
   }
 }
+__device__ __forceinline__ void get_angles(float2 (&c)[8], const float2* cs, int j, int lanes) {
+#pragma unroll
+  for (int m = 0; m < 8; m += 2) {
+    const float4 f = *reinterpret_cast<const float4*>(cs + (m * lanes + j * 2));
+    c[m] = make_float2(f.x, f.y);
+    c[m + 1] = make_float2(f.z, f.w);
+  }
+}
+
+// What forward and backward share: the units of this thread and its ring.
+template <typename T, int P, bool HALF, bool RING, int UPT>
+struct Units {
+  int j, lanes, d;
+  int head[UPT];
+  bool k_side[UPT], in[UPT];
+  uint32_t slot;
+
+  __device__ __forceinline__ Units(const QkArgs& a, int ops) {
+    lanes = a.lanes;
+    d = a.d;
+    j = threadIdx.x & (lanes - 1);
+#pragma unroll
+    for (int i = 0; i < UPT; ++i) {
+      const int h = ((int)threadIdx.x + i * (int)blockDim.x) / lanes;
+      k_side[i] = h >= a.heads[0];
+      head[i] = h - (k_side[i] ? a.heads[0] : 0);
+      in[i] = h < a.heads[0] + a.heads[1];
+    }
+    slot = (uint32_t)(ops * UPT * 16 * sizeof(T)) * blockDim.x;
+  }
+  template <typename V>
+  __device__ __forceinline__ V* at(V* const (&base)[2], const long long (&stride)[2], long long r, int i) const {
+    return (k_side[i] ? base[1] + r * stride[1] : base[0] + r * stride[0]) + head[i] * d;
+  }
+  __device__ __forceinline__ uint32_t place(int op, int i) const {
+    return (uint32_t)((op * UPT + i) * 16 * sizeof(T)) * blockDim.x;
+  }
+  __device__ __forceinline__ void clear(unsigned char* ring, int depth, int ops) const {
+    for (int s = 0; s < depth; ++s)
+      for (int o = 0; o < ops; ++o)
+#pragma unroll
+        for (int i = 0; i < UPT; ++i) clear16<T, P, HALF>(ring + s * slot + place(o, i), in[i], j, lanes, d);
+  }
+  __device__ __forceinline__ void weights(float (&w)[16], const QkArgs& a, int i) const {
+    const void* p = a.weight[k_side[i]];
+    const int off = a.norm == SPADE_QK_NORM_TOKEN ? head[i] * d : 0;
+    if (!p || !in[i]) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w[e] = 1.f;
+    } else if (a.weight_bf16) {
+      load16<bf16, P, HALF>(w, static_cast<const bf16*>(p) + off, true, j, lanes, d);
+    } else {
+      load16<float, P, HALF>(w, static_cast<const float*>(p) + off, true, j, lanes, d);
+    }
+  }
+};
 
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ void read_turns(Turns& tu, const QkArgs& a, float2* cs, int n) {
+  for (int i = threadIdx.x; i < a.pairs; i += blockDim.x) {
+    tu.turn[i] = a.turn[i];
+    tu.axis[i] = a.axis[i];
+  }
+  for (int i = threadIdx.x; i < n; i += blockDim.x) cs[i] = make_float2(1.f, 0.f);    // pairs that heads lack
+  __syncthreads();
+}
 
 // ---------------------------------------------------------------- forward --
-template <typename T, bool VEC, int UPT>
-__global__ void __launch_bounds__(UPT == 1 ? 512 : 1024, 1) qk_fwd_kernel(const __grid_constant__ QkArgs a) {
-  extern __shared__ float2 cs[];         // [2][kTok][d / 2]
-  __shared__ SumScratch<2 * kTok> sums;
-  const int lanes = a.lanes, j = threadIdx.x & (lanes - 1), head0 = threadIdx.x / lanes;
-  const int hstep = blockDim.x / lanes, nwarps = blockDim.x >> 5, d = a.d;
-  const bool half = a.half, own = VEC ? 16 * j < d : true;
-  int sh = 0, buf = 0;
-  for (long long r0 = (long long)blockIdx.x * kTok; r0 < a.rows; r0 += (long long)gridDim.x * kTok) {
-    const int n = (int)min((long long)kTok, a.rows - r0);
-    Share<VEC, T> x[kTok][2][UPT];
+template <typename T, int P, bool HALF, bool RING, int UPT, int K>
+__global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const __grid_constant__ QkArgs a, int depth) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ Turns tu;
+  __shared__ Scratch<K> sums;
+  __shared__ __align__(16) float2 cs[2][K * SPADE_ROPE_MAX_PAIRS];
+  const Units<T, P, HALF, RING, UPT> un(a, 1);
+  const int lanes = un.lanes, j = un.j, d = un.d, nwarps = blockDim.x >> 5;
+  const long long r0 = a.rows * blockIdx.x / gridDim.x, r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
+  const T* const xs[2] = {static_cast<const T*>(a.x[0]), static_cast<const T*>(a.x[1])};
+  T* const outs[2] = {static_cast<T*>(a.out[0]), static_cast<T*>(a.out[1])};
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  long long fr = r0;             // the next token to copy, its slot, and the slot of the next one to use
+  int fs = 0, us = 0;
+  auto fetch = [&]() {
+    if (fr < r1) {
 #pragma unroll
-    for (int k = 0; k < kTok; ++k)
+      for (int i = 0; i < UPT; ++i)
+        if constexpr (RING)
+          if (un.in[i]) fetch16<T, P, HALF>(ring_at + fs * un.slot + un.place(0, i), un.at(xs, a.x_stride, fr, i), j, lanes, d);
+    }
+    commit_async();
+    ++fr;
+    fs = fs + 1 == depth ? 0 : fs + 1;
+  };
+  if (RING) {
+    un.clear(ring, depth, 1);
+    for (int s = 0; s < depth; ++s) fetch();
+  }
+  float w[UPT][16];
+  const bool normed = a.norm != SPADE_QK_NORM_NONE, token = a.norm == SPADE_QK_NORM_TOKEN;
+  if (normed) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < UPT; ++i) un.weights(w[i], a, i);
+  }
+  read_turns(tu, a, cs[0], 2 * K * SPADE_ROPE_MAX_PAIRS);
+  angles<P, HALF, K>(a, tu, r0, r1, cs[0]);
+  int half = 0, buf = 0;
+  auto get = [&](float (&v)[16], const unsigned char* at, long long r, int i) {
+    if constexpr (RING) ring16<T, P>(v, at + un.place(0, i));
+    else load16<T, P, HALF>(v, un.at(xs, a.x_stride, r, i), un.in[i], j, lanes, d);
+  };
+  for (long long r = r0; r < r1; r += K) {
+    const int n = r1 - r < K ? (int)(r1 - r) : K;
+    if (RING) wait_async_upto(depth - K);
+    const unsigned char* at[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) at[k] = ring + (us + k >= depth ? us + k - depth : us + k) * un.slot;
+    float s[2 * K], rs[K][UPT];
+    if (normed) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        s[k] = s[K + k] = 0.f;
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-          const int h = head0 + i * hstep;
-          const bool in = k < n && own && h < a.heads[t];
-          x[k][t][i].load(static_cast<const T*>(a.x[t]) + (r0 + k) * a.x_stride[t] + (long long)h * d, in, j, lanes,
-                          half, d);
-        }
-    float2* c = cs + buf * (kTok * (d >> 1));
-    angles(a, r0, n, c);
-    float s[2 * kTok];
-    float rs[kTok][2][UPT];
-    if (a.norm != SPADE_QK_NORM_NONE) {
+          float v[16], q = 0.f;
+          if (k < n) {
+            get(v, at[k], r + k, i);
 #pragma unroll
-      for (int k = 0; k < kTok; ++k)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          s[2 * k + t] = 0.f;
-#pragma unroll
-          for (int i = 0; i < UPT; ++i) {
-            float u[8], v[8], q = 0.f;
-            x[k][t][i].get(u, v, half);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q += u[e] * u[e] + v[e] * v[e];
-            s[2 * k + t] += q;
-            rs[k][t][i] = q;
+            for (int e = 0; e < 16; ++e) q += v[e] * v[e];
           }
-        }
-    }
-    if (a.norm == SPADE_QK_NORM_TOKEN && nwarps > 1) {
-      block_sum(s, sums, sh, nwarps);      // its barrier also covers the angles
-    } else {
-      if (a.norm == SPADE_QK_NORM_TOKEN) block_sum(s, sums, sh, nwarps);
-      __syncthreads();
-    }
-#pragma unroll
-    for (int k = 0; k < kTok; ++k)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-          if (a.norm == SPADE_QK_NORM_TOKEN)
-            rs[k][t][i] = rsqrtf(s[2 * k + t] / (float)(a.heads[t] * d) + a.eps);
-          else if (a.norm == SPADE_QK_NORM_HEAD)
-            rs[k][t][i] = rsqrtf(lanes_sum(rs[k][t][i], lanes) / (float)d + a.eps);
-          else
-            rs[k][t][i] = 1.f;
-        }
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < UPT; ++i) {
-        const int h = head0 + i * hstep;
-        const bool in = own && h < a.heads[t];
-        float wa[8], wb[8];
-        load_weight<VEC>(wa, wb, a.weight[t], a.weight_bf16, a.norm == SPADE_QK_NORM_TOKEN ? h * d : 0, in, j, lanes,
-                         half, d);
-#pragma unroll
-        for (int k = 0; k < kTok; ++k) {
-          if (!in || k >= n) continue;
-          float u[8], v[8];
-          x[k][t][i].get(u, v, half);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int p = pair_of<VEC>(j, e, lanes);
-            const float2 r = p < (d >> 1) ? c[k * (d >> 1) + p] : make_float2(1.f, 0.f);
-            const float p0 = u[e] * (rs[k][t][i] * wa[e]), p1 = v[e] * (rs[k][t][i] * wb[e]);
-            u[e] = p0 * r.x - p1 * r.y;
-            v[e] = p0 * r.y + p1 * r.x;
-          }
-          store_share<VEC>(static_cast<T*>(a.out[t]) + (r0 + k) * a.out_stride[t] + (long long)h * d, u, v, j, lanes,
-                           half, d);
+          if (un.k_side[i]) s[K + k] += q;
+          else s[k] += q;
+          rs[k][i] = q;
         }
       }
+    }
+    if (token && nwarps > 1) {
+      block_sum(s, sums, half, nwarps);          // its barrier also covers the angles
+    } else {
+      __syncthreads();
+      if (token) block_sum(s, sums, half, nwarps);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        if (token) rs[k][i] = rsqrtf((un.k_side[i] ? s[K + k] : s[k]) / (float)(a.heads[un.k_side[i]] * d) + a.eps);
+        else if (normed) rs[k][i] = rsqrtf(lanes_sum(rs[k][i], lanes) / (float)d + a.eps);
+      }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k >= n) break;
+      float2 c[8];
+      get_angles(c, cs[buf] + k * 8 * lanes, j, lanes);
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        if (!un.in[i]) continue;
+        float v[16];
+        get(v, at[k], r + k, i);
+        if (normed) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] *= rs[k][i] * w[i][e];
+        }
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          const float p0 = v[first_of<HALF>(m)], p1 = v[second_of<HALF>(m)];
+          v[first_of<HALF>(m)] = p0 * c[m].x - p1 * c[m].y;
+          v[second_of<HALF>(m)] = p0 * c[m].y + p1 * c[m].x;
+        }
+        store16<T, P, HALF>(un.at(outs, a.out_stride, r + k, i), v, j, lanes, d);
+      }
+    }
+    if (RING) {
+      for (int k = 0; k < n; ++k) fetch();
+      us = us + n >= depth ? us + n - depth : us + n;
+    }
     buf ^= 1;
+    if (r + K < r1) angles<P, HALF, K>(a, tu, r + K, r1, cs[buf]);    // last read before this token's barrier
   }
+  if (RING) wait_async<0>();
 }
 
 // --------------------------------------------------------------- backward --
-template <typename T, bool VEC, int UPT>
-__global__ void __launch_bounds__(UPT == 1 ? 512 : 1024, 1) qk_bwd_kernel(const __grid_constant__ QkArgs a) {
-  extern __shared__ float2 cs[];         // [2][d / 2]
-  __shared__ SumScratch<4> sums;
-  const int lanes = a.lanes, j = threadIdx.x & (lanes - 1), head0 = threadIdx.x / lanes;
-  const int hstep = blockDim.x / lanes, nwarps = blockDim.x >> 5, d = a.d;
-  const bool half = a.half, own = VEC ? 16 * j < d : true;
+template <typename T, int P, bool HALF, bool RING, int UPT, int K>
+__global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const __grid_constant__ QkArgs a, int depth) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ Turns tu;
+  __shared__ Scratch<2 * K> sums;
+  __shared__ __align__(16) float2 cs[2][K * SPADE_ROPE_MAX_PAIRS];
   const bool normed = a.norm != SPADE_QK_NORM_NONE, token = a.norm == SPADE_QK_NORM_TOKEN;
-  int sh = 0, buf = 0;
-  float dw[2][UPT][2][8];
+  const int ops = normed ? 2 : 1;
+  const Units<T, P, HALF, RING, UPT> un(a, ops);
+  const int lanes = un.lanes, j = un.j, d = un.d, nwarps = blockDim.x >> 5;
+  const long long r0 = a.rows * blockIdx.x / gridDim.x, r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
+  const T* const gs[2] = {static_cast<const T*>(a.dout[0]), static_cast<const T*>(a.dout[1])};
+  const T* const xs[2] = {static_cast<const T*>(a.x[0]), static_cast<const T*>(a.x[1])};
+  T* const outs[2] = {static_cast<T*>(a.out[0]), static_cast<T*>(a.out[1])};
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  long long fr = r0;
+  int fs = 0, us = 0;
+  auto fetch = [&]() {
+    if (fr < r1) {
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int i = 0; i < UPT; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dw[t][i][0][e] = dw[t][i][1][e] = 0.f;
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    Share<VEC, T> x[2][UPT], g[2][UPT];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < UPT; ++i) {
-        const int h = head0 + i * hstep;
-        const bool in = own && h < a.heads[t];
-        g[t][i].load(static_cast<const T*>(a.dout[t]) + r * a.dout_stride[t] + (long long)h * d, in, j, lanes, half, d);
-        if (normed)
-          x[t][i].load(static_cast<const T*>(a.x[t]) + r * a.x_stride[t] + (long long)h * d, in, j, lanes, half, d);
-      }
-    float2* c = cs + buf * (d >> 1);
-    angles(a, r, 1, c);
-    __syncthreads();
-    float ua[2][UPT][8], ub[2][UPT][8];
-    float s[4] = {0.f, 0.f, 0.f, 0.f};       // per tensor: sum of x^2, sum of w u x
-    float hs[2][UPT][2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < UPT; ++i) {
-        const int h = head0 + i * hstep;
-        const bool in = own && h < a.heads[t];
-        float xa[8], xb[8], wa[8], wb[8];
-        g[t][i].get(ua[t][i], ub[t][i], half);
-        if (normed) x[t][i].get(xa, xb, half);
-        load_weight<VEC>(wa, wb, normed ? a.weight[t] : nullptr, a.weight_bf16, token ? h * d : 0, in, j, lanes, half,
-                         d);
-        float q0 = 0.f, q1 = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int p = pair_of<VEC>(j, e, lanes);
-          const float2 r2 = p < (d >> 1) ? c[p] : make_float2(1.f, 0.f);
-          const float p0 = ua[t][i][e], p1 = ub[t][i][e];
-          ua[t][i][e] = p0 * r2.x + p1 * r2.y;
-          ub[t][i][e] = p1 * r2.x - p0 * r2.y;
-          if (normed) {
-            q0 += xa[e] * xa[e] + xb[e] * xb[e];
-            q1 += (ua[t][i][e] * wa[e]) * xa[e] + (ub[t][i][e] * wb[e]) * xb[e];
+      for (int i = 0; i < UPT; ++i)
+        if constexpr (RING)
+          if (un.in[i]) {
+            const uint32_t to = ring_at + fs * un.slot;
+            fetch16<T, P, HALF>(to + un.place(0, i), un.at(gs, a.dout_stride, fr, i), j, lanes, d);
+            if (normed) fetch16<T, P, HALF>(to + un.place(1, i), un.at(xs, a.x_stride, fr, i), j, lanes, d);
           }
-        }
-        s[2 * t] += q0;
-        s[2 * t + 1] += q1;
-        hs[t][i][0] = q0;
-        hs[t][i][1] = q1;
-      }
-    if (token) block_sum(s, sums, sh, nwarps);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < UPT; ++i) {
-        const int h = head0 + i * hstep;
-        const bool in = own && h < a.heads[t];
-        if (normed) {      // absent heads hold zeros, and stay out of dw whatever eps makes of them
-          float q0 = s[2 * t], q1 = s[2 * t + 1];
-          float inv = 1.f / (float)(token ? a.heads[t] * d : d);
-          if (!token) {
-            q0 = lanes_sum(hs[t][i][0], lanes);
-            q1 = lanes_sum(hs[t][i][1], lanes);
-          }
-          const float rs = rsqrtf(q0 * inv + a.eps);
-          const float k = rs * rs * q1 * inv;
-          float xa[8], xb[8], wa[8], wb[8];
-          x[t][i].get(xa, xb, half);
-          load_weight<VEC>(wa, wb, a.weight[t], a.weight_bf16, token ? h * d : 0, in, j, lanes, half, d);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (in) {
-              dw[t][i][0][e] += ua[t][i][e] * (xa[e] * rs);
-              dw[t][i][1][e] += ub[t][i][e] * (xb[e] * rs);
-            }
-            ua[t][i][e] = rs * (ua[t][i][e] * wa[e] - xa[e] * k);
-            ub[t][i][e] = rs * (ub[t][i][e] * wb[e] - xb[e] * k);
-          }
-        }
-        if (in)
-          store_share<VEC>(static_cast<T*>(a.out[t]) + r * a.out_stride[t] + (long long)h * d, ua[t][i], ub[t][i], j,
-                           lanes, half, d);
-      }
-    buf ^= 1;
+    }
+    commit_async();
+    ++fr;
+    fs = fs + 1 == depth ? 0 : fs + 1;
+  };
+  if (RING) {
+    un.clear(ring, depth, ops);
+    for (int s = 0; s < depth; ++s) fetch();
   }
+  float w[UPT][16], dw[UPT][16];
+#pragma unroll
+  for (int i = 0; i < UPT; ++i) {
+    if (normed) un.weights(w[i], a, i);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) dw[i][e] = 0.f;
+  }
+  read_turns(tu, a, cs[0], 2 * K * SPADE_ROPE_MAX_PAIRS);
+  angles<P, HALF, K>(a, tu, r0, r1, cs[0]);
+  int half = 0, buf = 0;
+  auto get_g = [&](float (&v)[16], const unsigned char* at, long long r, int i, const float2 (&c)[8]) {
+    if constexpr (RING) ring16<T, P>(v, at + un.place(0, i));
+    else load16<T, P, HALF>(v, un.at(gs, a.dout_stride, r, i), un.in[i], j, lanes, d);
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const float p0 = v[first_of<HALF>(m)], p1 = v[second_of<HALF>(m)];
+      v[first_of<HALF>(m)] = p0 * c[m].x + p1 * c[m].y;
+      v[second_of<HALF>(m)] = p1 * c[m].x - p0 * c[m].y;
+    }
+  };
+  auto get_x = [&](float (&v)[16], const unsigned char* at, long long r, int i) {
+    if constexpr (RING) ring16<T, P>(v, at + un.place(1, i));
+    else load16<T, P, HALF>(v, un.at(xs, a.x_stride, r, i), un.in[i], j, lanes, d);
+  };
+  for (long long r = r0; r < r1; r += K) {
+    const int n = r1 - r < K ? (int)(r1 - r) : K;
+    if (RING) wait_async_upto(depth - K);
+    __syncthreads();                             // the angles are there
+    const unsigned char* at[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) at[k] = ring + (us + k >= depth ? us + k - depth : us + k) * un.slot;
+    // per token and tensor: sum of x^2, sum of w u x; then 1 / deviation and rstd^2 mean(w u x)
+    float s[4 * K], rs[K][UPT], cf[K][UPT];
+    if (normed) {
+#pragma unroll
+      for (int i = 0; i < 4 * K; ++i) s[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float2 c[8];
+        get_angles(c, cs[buf] + k * 8 * lanes, j, lanes);
+#pragma unroll
+        for (int i = 0; i < UPT; ++i) {
+          float q0 = 0.f, q1 = 0.f;
+          if (k < n) {
+            float x[16], u[16];
+            get_x(x, at[k], r + k, i);
+            get_g(u, at[k], r + k, i, c);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              q0 += x[e] * x[e];
+              q1 += (u[e] * w[i][e]) * x[e];
+            }
+          }
+          if (un.k_side[i]) {
+            s[K + k] += q0;
+            s[3 * K + k] += q1;
+          } else {
+            s[k] += q0;
+            s[2 * K + k] += q1;
+          }
+          rs[k][i] = q0;
+          cf[k][i] = q1;
+        }
+      }
+      if (token) block_sum(s, sums, half, nwarps);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < UPT; ++i) {
+          const bool ks = un.k_side[i];
+          const float q0 = token ? (ks ? s[K + k] : s[k]) : lanes_sum(rs[k][i], lanes);
+          const float q1 = token ? (ks ? s[3 * K + k] : s[2 * K + k]) : lanes_sum(cf[k][i], lanes);
+          const float inv = 1.f / (float)(token ? a.heads[ks] * d : d);
+          rs[k][i] = rsqrtf(q0 * inv + a.eps);
+          cf[k][i] = rs[k][i] * rs[k][i] * q1 * inv;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k >= n) break;
+      float2 c[8];
+      get_angles(c, cs[buf] + k * 8 * lanes, j, lanes);
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        if (!un.in[i]) continue;                 // absent heads stay out of dw whatever eps makes of their zeros
+        float u[16];
+        get_g(u, at[k], r + k, i, c);
+        if (normed) {
+          float x[16];
+          get_x(x, at[k], r + k, i);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            dw[i][e] += u[e] * (x[e] * rs[k][i]);
+            u[e] = rs[k][i] * (u[e] * w[i][e] - x[e] * cf[k][i]);
+          }
+        }
+        store16<T, P, HALF>(un.at(outs, a.out_stride, r + k, i), u, j, lanes, d);
+      }
+    }
+    if (RING) {
+      for (int k = 0; k < n; ++k) fetch();
+      us = us + n >= depth ? us + n - depth : us + n;
+    }
+    buf ^= 1;
+    if (r + K < r1) angles<P, HALF, K>(a, tu, r + K, r1, cs[buf]);    // last read before this token's barrier
+  }
+  if (RING) wait_async<0>();
   if (!normed || !a.part) return;
   // this block's weight sums: [heads * d] of Q then of K, or (per-head norm)
-  // [d] of each, its heads added in head order
+  // [d] of each, its heads added in a fixed order
   float* part = a.part + (long long)blockIdx.x * (token ? (a.heads[0] + a.heads[1]) * d : 2 * d);
   if (token) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < UPT; ++i)
+      if (un.in[i]) {
+        float* o = part + ((un.k_side[i] ? a.heads[0] : 0) + un.head[i]) * d;
 #pragma unroll
-      for (int i = 0; i < UPT; ++i) {
-        const int h = head0 + i * hstep;
-        if (own && h < a.heads[t]) {
-          float* o = part + (t ? a.heads[0] * d : 0) + h * d;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int p = pair_of<VEC>(j, e, lanes);
-            if (p < (d >> 1)) {
-              o[first_of(p, half)] = dw[t][i][0][e];
-              o[second_of(p, half, d)] = dw[t][i][1][e];
-            }
-          }
-        }
+        for (int e = 0; e < 16; ++e)
+          if (owned<P, HALF>(j, lanes, e, d)) o[channel<P, HALF>(j, lanes, e, d)] = dw[i][e];
       }
     return;
   }
-  __shared__ float heads_part[32][256];
+  float* by_warp = reinterpret_cast<float*>(ring);       // [warps][d]
   for (int t = 0; t < 2; ++t) {
+    __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < 16; ++e) {
+      float v = 0.f;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < UPT; ++i) v += dw[t][i][k][e];
-        // the heads of one warp, then the warps through shared memory
-        for (int o = lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int p = pair_of<VEC>(j, e, lanes);
-        if ((int)(threadIdx.x & 31) < lanes && p < (d >> 1))
-          heads_part[threadIdx.x >> 5][k ? second_of(p, half, d) : first_of(p, half)] = v;
-      }
+      for (int i = 0; i < UPT; ++i) v += un.k_side[i] == (t == 1) ? dw[i][e] : 0.f;
+      // the heads of one warp, then the warps through shared memory
+      for (int o = lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if ((int)(threadIdx.x & 31) < lanes && owned<P, HALF>(j, lanes, e, d))
+        by_warp[(threadIdx.x >> 5) * d + channel<P, HALF>(j, lanes, e, d)] = v;
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
       float v = 0.f;
-      for (int w = 0; w < nwarps; ++w) v += heads_part[w][i];
+      for (int wp = 0; wp < nwarps; ++wp) v += by_warp[wp * d + i];
       part[t * d + i] = v;
     }
-    __syncthreads();
   }
 }
 
@@ -434,43 +515,71 @@ __global__ void __launch_bounds__(1024) qk_reduce_kernel(const float* part, int 
 }
 
 // ----------------------------------------------------------------- launch --
-int most_heads(const QkArgs& a) { return a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1]; }
-
-// A thread takes one head's share of a token, or two where a block of 512
-// threads would not cover the heads.
-int units_per_thread(const QkArgs& a) { return most_heads(a) * a.lanes <= 512 ? 1 : 2; }
+// Two units a thread, or four where 512 threads of two would not cover them.
+int units_per_thread(const QkArgs& a) { return (a.heads[0] + a.heads[1]) * a.lanes <= 1024 ? 2 : 4; }
 int block_threads(const QkArgs& a) {
   const int upt = units_per_thread(a);
-  const int t = (most_heads(a) * a.lanes + upt - 1) / upt;
-  return (t + 31) / 32 * 32;
+  return (((a.heads[0] + a.heads[1]) * a.lanes + upt - 1) / upt + 31) / 32 * 32;
 }
 
-int bwd_grid(const QkArgs& a) {
-  const int t = block_threads(a);
-  const long long resident = (long long)num_sms() * (t > 512 ? 1 : (t > 256 ? 2 : (t > 128 ? 4 : 8)));
-  return (int)(a.rows < resident ? a.rows : resident);
+constexpr int kSmemSm = 227 * 1024;
+constexpr int kStatic = sizeof(Turns) + sizeof(Scratch<4>) + 4 * SPADE_ROPE_MAX_PAIRS * sizeof(float2) + 1024 + 64;
+
+// Blocks of an SM: by registers (96 a thread forward, 128 backward), and so
+// that `least` tokens a block fit in shared memory.
+int blocks_of(int threads, int sm_threads, size_t slot, int least) {
+  int b = sm_threads / threads;
+  const int fit = (int)(kSmemSm / (slot * least + kStatic));
+  b = b < fit ? b : fit;
+  return b < 1 ? 1 : (b > 8 ? 8 : b);
+}
+int grid_of(const QkArgs& a, int blocks, int k) {
+  const long long resident = (long long)num_sms() * blocks, most = (a.rows + k - 1) / k;
+  return (int)(most < resident ? most : resident);
 }
 
-template <typename T, bool VEC>
-cudaError_t run_fwd(const QkArgs& a, cudaStream_t s) {
-  const int upt = units_per_thread(a), threads = block_threads(a);
-  const long long tiles = (a.rows + kTok - 1) / kTok;
-  const long long resident = (long long)num_sms() * (threads > 512 ? 1 : (1024 / threads > 16 ? 16 : 1024 / threads));
-  const int grid = (int)(tiles < resident ? tiles : resident);
-  const size_t smem = 2 * kTok * (a.d / 2) * sizeof(float2);
-  if (upt == 1) qk_fwd_kernel<T, VEC, 1><<<grid, threads, smem, s>>>(a);
-  else qk_fwd_kernel<T, VEC, 2><<<grid, threads, smem, s>>>(a);
+template <typename K>
+cudaError_t launch(K kernel, const QkArgs& a, int grid, int threads, int blocks, int k, size_t slot, bool ring,
+                   size_t least, cudaStream_t s) {
+  int depth = 0;
+  size_t smem = 0;
+  if (ring) {
+    const size_t room = kSmemSm / blocks - kStatic;
+    const long long rows = (a.rows + grid - 1) / grid;
+    depth = (int)(room / slot < kDepthMax ? room / slot : kDepthMax);
+    if (rows < depth) depth = (int)(rows > k ? rows : k);
+    if (depth < k) return cudaErrorInvalidConfiguration;
+    smem = depth * slot;
+  }
+  if (smem < least) smem = least;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, threads, smem, s>>>(a, depth);
   return cudaGetLastError();
 }
 
-template <typename T, bool VEC>
+template <typename T, int P, bool HALF, bool RING, int UPT>
+cudaError_t run_fwd(const QkArgs& a, cudaStream_t s) {
+  constexpr int K = 2;
+  const int threads = block_threads(a);
+  const size_t slot = (size_t)threads * UPT * 16 * sizeof(T);
+  const int blocks = blocks_of(threads, 640, RING ? slot : 0, K);
+  return launch(qk_fwd_kernel<T, P, HALF, RING, UPT, K>, a, grid_of(a, blocks, K), threads, blocks, K, slot, RING, 0, s);
+}
+
+// Blocks of an SM of the backward pass at most (bfloat16 rows).
+int bwd_blocks(const QkArgs& a) { return blocks_of(block_threads(a), 512, 0, 0); }
+
+template <typename T, int P, bool HALF, bool RING, int UPT>
 cudaError_t run_bwd(const QkArgs& a, cudaStream_t s) {
-  const int upt = units_per_thread(a), threads = block_threads(a);
-  const size_t smem = 2 * (a.d / 2) * sizeof(float2);
-  const int grid = bwd_grid(a);
-  if (upt == 1) qk_bwd_kernel<T, VEC, 1><<<grid, threads, smem, s>>>(a);
-  else qk_bwd_kernel<T, VEC, 2><<<grid, threads, smem, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  constexpr int K = sizeof(T) == 2 ? 2 : 1;
+  const int threads = block_threads(a);
+  const size_t slot = (size_t)threads * UPT * 16 * sizeof(T) * (a.norm != SPADE_QK_NORM_NONE ? 2 : 1);
+  const size_t least = a.norm == SPADE_QK_NORM_HEAD ? (size_t)(threads / 32) * a.d * sizeof(float) : 0;
+  const int blocks = blocks_of(threads, 512, RING ? slot : 0, K == 1 ? 3 : K), grid = grid_of(a, blocks, K);
+  cudaError_t e = launch(qk_bwd_kernel<T, P, HALF, RING, UPT, K>, a, grid, threads, blocks, K, slot, RING, least, s);
   if (e != cudaSuccess || !a.part) return e;
   const bool token = a.norm == SPADE_QK_NORM_TOKEN;
   const int wq = token ? a.heads[0] * a.d : a.d, wk = token ? a.heads[1] * a.d : a.d;
@@ -478,21 +587,55 @@ cudaError_t run_bwd(const QkArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Threads of four units read tokens where they are used: two tokens of so
+// many channels need not fit in shared memory.
+template <typename T, int P, bool RING>
+cudaError_t by_shape(const QkArgs& a, bool back, cudaStream_t s) {
+  const bool two = units_per_thread(a) == 2;
+  if (back) {
+    if (a.half) return two ? run_bwd<T, P, true, RING, 2>(a, s) : run_bwd<T, P, true, false, 4>(a, s);
+    return two ? run_bwd<T, P, false, RING, 2>(a, s) : run_bwd<T, P, false, false, 4>(a, s);
+  }
+  if (a.half) return two ? run_fwd<T, P, true, RING, 2>(a, s) : run_fwd<T, P, true, false, 4>(a, s);
+  return two ? run_fwd<T, P, false, RING, 2>(a, s) : run_fwd<T, P, false, false, 4>(a, s);
+}
+
+// The widest piece, in channels, that heads (halves of heads) and every row
+// allow: 16 bytes, 4 bytes, or a single channel.
+int piece_of(const QkArgs& a, int size) {
+  for (int p = 16 / size; p > 1; p = p > 2 ? 2 : 1) {
+    bool ok = a.d % (a.half ? 2 * p : p) == 0;
+    for (int t = 0; t < 2; ++t) {
+      const struct { const void* p; long long stride; int size; } ops[] = {
+          {a.x[t], a.x_stride[t], size}, {a.dout[t], a.dout_stride[t], size}, {a.out[t], a.out_stride[t], size},
+          {a.weight[t], 0, a.weight_bf16 ? 2 : 4}};
+      for (const auto& o : ops) {
+        const int need = p * o.size < 16 ? p * o.size : 16;
+        ok = ok && (!o.p || (reinterpret_cast<uintptr_t>(o.p) % need == 0 && o.stride % p == 0));
+      }
+    }
+    if (ok) return p;
+  }
+  return 1;
+}
+
+cudaError_t run(const QkArgs& a, bool is_bf16, bool back, cudaStream_t s) {
+  const int p = piece_of(a, is_bf16 ? 2 : 4);
+  if (is_bf16) {
+    if (p == 8) return by_shape<bf16, 8, true>(a, back, s);
+    return p == 2 ? by_shape<bf16, 2, true>(a, back, s) : by_shape<bf16, 1, false>(a, back, s);
+  }
+  return p == 4 ? by_shape<float, 4, true>(a, back, s) : by_shape<float, 1, true>(a, back, s);
+}
+
 }  // namespace
 
 size_t qk_bwd_floats(const QkArgs& a) {
   if (a.norm == SPADE_QK_NORM_NONE) return 0;
-  return (size_t)bwd_grid(a) * (a.norm == SPADE_QK_NORM_TOKEN ? (a.heads[0] + a.heads[1]) * a.d : 2 * a.d);
+  return (size_t)grid_of(a, bwd_blocks(a), 1) * (a.norm == SPADE_QK_NORM_TOKEN ? (a.heads[0] + a.heads[1]) * a.d : 2 * a.d);
 }
 
-cudaError_t launch_qk_fwd(const QkArgs& a, bool bf16, cudaStream_t s) {
-  if (bf16) return a.vec ? run_fwd<__nv_bfloat16, true>(a, s) : run_fwd<__nv_bfloat16, false>(a, s);
-  return a.vec ? run_fwd<float, true>(a, s) : run_fwd<float, false>(a, s);
-}
-
-cudaError_t launch_qk_bwd(const QkArgs& a, bool bf16, cudaStream_t s) {
-  if (bf16) return a.vec ? run_bwd<__nv_bfloat16, true>(a, s) : run_bwd<__nv_bfloat16, false>(a, s);
-  return a.vec ? run_bwd<float, true>(a, s) : run_bwd<float, false>(a, s);
-}
+cudaError_t launch_qk_fwd(const QkArgs& a, bool is_bf16, cudaStream_t s) { return run(a, is_bf16, false, s); }
+cudaError_t launch_qk_bwd(const QkArgs& a, bool is_bf16, cudaStream_t s) { return run(a, is_bf16, true, s); }
 
 }  // namespace spade

@@ -1,0 +1,379 @@
+// Gradients of the row passes (spade_norm_modulate_bwd,
+// spade_gate_residual_bwd, spade_gate_residual_norm_bwd).  With A_g = sum of
+// dh and B_g = sum of dh * xhat over the rows of group g, C_g = sum of
+// dx' * yhat:
+//   dshift = A, dscale = w B + b A, dw = sum_g (1 + scale_g) B_g,
+//   db = sum_g (1 + scale_g) A_g, dgate = r pw C, dpw = r sum_g gate_g C_g,
+// so three column sums serve every parameter, and
+//   u = dh (1 + scale) w,  dx = dx' + rstd (u - mean(u) - xhat mean(u xhat))
+// (the mean(u) term for the layer norm only), dy likewise through P.
+//
+// A block works on units, runs of rows of one modulation group: the column
+// sums stay in registers until the unit ends, then go to the workspace, and a
+// second small launch adds them in a fixed order, in float64: no atomics, the
+// same result on every run.  Rows are walked K at a time, read again from the
+// ring where a later step needs them.  Bound by memory: each row is read and
+// written once.
+#pragma once
+#include "row_pass.cuh"
+
+namespace spade {
+namespace {
+
+using namespace rowpass;
+
+// A unit is chunk c of group g: rows [g R + R c / C, g R + R (c + 1) / C) of a
+// group of R rows cut into C chunks.
+struct Cursor {
+  long long unit, r, end;
+
+  __device__ __forceinline__ void enter(const RowArgs& a, long long u) {
+    unit = u;
+    if (a.chunks == 1) {
+      r = u * a.rows_per_group;
+      end = r + a.rows_per_group;
+    } else {
+      const long long g = u / a.chunks, c = u - g * a.chunks, base = g * a.rows_per_group;
+      r = base + a.rows_per_group * c / a.chunks;
+      end = base + a.rows_per_group * (c + 1) / a.chunks;
+    }
+  }
+};
+
+// With C > 1 a unit's sums A, B, C go to `part` [unit][3][dim] and
+// row_reduce_kernel makes every parameter gradient of them.  With C = 1 a unit
+// is a whole group: its modulation gradients are final and written here, and
+// the weights' sums are added up over the block's units in `part`
+// [block][3][dim].
+template <typename XT, typename BT, int P, bool RING, int NV, int K, bool RES, bool NORM>
+__global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
+    row_bwd_kernel(const __grid_constant__ RowArgs a, int depth, bool weights) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ Shared<K> sh;
+  const int dim = a.dim, nwarps = blockDim.x >> 5;
+  const bool post = RES && a.post_norm != kNone, grad = a.dx_out != nullptr;
+  const uint32_t xb = slot_bytes(blockDim.x, NV, sizeof(XT)), bb = slot_bytes(blockDim.x, NV, sizeof(BT));
+  Stream<XT, P, RING, NV> sg{static_cast<const XT*>(a.dx_out), a.dx_out_stride, 0};
+  Stream<BT, P, RING, NV> sy{static_cast<const BT*>(a.y), a.y_stride, xb};
+  Stream<XT, P, RING, NV> sx{static_cast<const XT*>(a.x), a.x_stride, xb + (RES ? bb : 0)};
+  Stream<BT, P, RING, NV> sd{static_cast<const BT*>(a.dh), a.dh_stride, sx.at + xb};
+  const uint32_t slot = NORM ? sd.at + bb : sx.at;
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  const long long units = a.groups * a.chunks;
+
+  Cursor f;                      // the next row to copy
+  int fs = 0, us = 0;            // its slot; the slot of the next row to use
+  f.enter(a, blockIdx.x);
+  auto fetch = [&]() {
+    if (f.unit < units) {
+      const uint32_t to = ring_at + fs * slot;
+      if (grad) sg.fetch(to, f.r, dim);
+      if (RES) sy.fetch(to, f.r, dim);
+      if (NORM) {
+        sx.fetch(to, f.r, dim);
+        sd.fetch(to, f.r, dim);
+      }
+      if (++f.r == f.end && f.unit + gridDim.x < units) f.enter(a, f.unit + gridDim.x);
+      else if (f.r == f.end) f.unit = units;
+    }
+    commit_async();
+    fs = fs + 1 == depth ? 0 : fs + 1;
+  };
+  if (RING) {
+    for (int d = 0; d < depth; ++d) {
+      unsigned char* p = ring + d * slot;
+      if (grad) sg.clear(p, dim);
+      if (RES) sy.clear(p, dim);
+      if (NORM) {
+        sx.clear(p, dim);
+        sd.clear(p, dim);
+      }
+      fetch();
+    }
+  }
+  count_columns<P, NV>(sh.count, dim);
+  int half = 0;
+  bool first = true;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    Cursor c;
+    c.enter(a, u);
+    const long long g = a.chunks == 1 ? u : u / a.chunks;
+    float gate[NV][8], mul[NV][8];     // r gate pw, and (1 + s) w
+    float A[NV][8], B[NV][8], C[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float t[8];
+      if (RES) {
+        load_param<P>(gate[i], a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
+        load_param<P>(t, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gate[i][e] *= a.residual_scale * t[e];
+      }
+      if (NORM) {
+        load_param<P>(mul[i], a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
+        load_param<P>(t, a.weight, 0, a.param_bf16, 1.f, i, dim);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mul[i][e] = (1.f + mul[i][e]) * t[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) A[i][e] = B[i][e] = C[i][e] = 0.f;
+    }
+    for (long long r = c.r; r < c.end;) {
+      const int n = c.end - r < K ? (int)(c.end - r) : K;
+      if (RING) wait_async_upto(depth - K);
+      const unsigned char* at[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int s = us + k >= depth ? us + k - depth : us + k;
+        at[k] = ring + s * slot;
+      }
+      float v[K][NV][8];               // x', then the gradient that reaches P
+      float ym[K], ys[K];
+      auto get_yhat = [&](float (&y)[8], int k, int i) {
+        sy.get(y, at[k], r + k, i, dim);
+        if (post) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = column<P>(i, e) < dim ? (y[e] - ym[k]) * ys[k] : 0.f;
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[k][i][e] = 0.f;
+      if (post) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (k < n) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) sy.get(v[k][i], at[k], r + k, i, dim);
+          }
+        row_stats<P, NV, K>(v, a.post_norm, a.post_eps, dim, sh, half, nwarps, ym, ys);
+      }
+      float xm[K], xs[K], m0[K], m1[K];
+      if (NORM) {
+        float w[K][NV][8];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (k < n) {
+              sx.get(v[k][i], at[k], r + k, i, dim);
+              if (RES) {
+                float y[8];
+                get_yhat(y, k, i);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[k][i][e] += gate[i][e] * y[e];
+              }
+              sd.get(w[k][i], at[k], r + k, i, dim);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[k][i][e] *= mul[i][e];
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[k][i][e] = 0.f;
+            }
+          }
+        row_stats_bwd<P, NV, K>(v, w, a.norm, a.eps, dim, sh, half, nwarps, xm, xs, m0, m1);
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (k >= n) break;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float gr[8];
+          if (grad) {
+            sg.get(gr, at[k], r + k, i, dim);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) gr[e] = 0.f;
+          }
+          if (NORM) {
+            float dh[8];
+            sd.get(dh, at[k], r + k, i, dim);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float xh = (v[k][i][e] - xm[k]) * xs[k];
+              A[i][e] += dh[e];
+              B[i][e] += dh[e] * xh;
+              gr[e] += xs[k] * (dh[e] * mul[i][e] - m0[k] - xh * m1[k]);
+            }
+            store8<P>(static_cast<XT*>(a.dx) + (r + k) * a.dx_stride, gr, i, dim);
+          }
+          if (RES) {
+            float y[8];
+            get_yhat(y, k, i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              C[i][e] += gr[e] * y[e];
+              v[k][i][e] = column<P>(i, e) < dim ? gr[e] * gate[i][e] : 0.f;
+            }
+            if (!post) store8<P>(static_cast<BT*>(a.dy) + (r + k) * a.dy_stride, v[k][i], i, dim);
+          }
+        }
+      }
+      if (post) {
+        float t[2 * K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          t[k] = t[K + k] = 0.f;
+          if (k < n) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+              float y[8];
+              get_yhat(y, k, i);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                t[k] += v[k][i][e];
+                t[K + k] += v[k][i][e] * y[e];
+              }
+            }
+          }
+        }
+        block_sum(t, sh.sums, half, nwarps);
+        const float inv_dim = 1.f / (float)dim;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (k >= n) break;
+          const float p0 = a.post_norm == kLayer ? t[k] * inv_dim : 0.f, p1 = t[K + k] * inv_dim;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            float y[8];
+            get_yhat(y, k, i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = ys[k] * (v[k][i][e] - p0 - y[e] * p1);
+            store8<P>(static_cast<BT*>(a.dy) + (r + k) * a.dy_stride, y, i, dim);
+          }
+        }
+      }
+      if (RING) {
+        for (int k = 0; k < n; ++k) fetch();
+        us = us + n >= depth ? us + n - depth : us + n;
+      }
+      r += n;
+    }
+    if (a.chunks > 1) {
+      float* p = a.part + u * 3 * dim;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (NORM) {
+          store8<P>(p, A[i], i, dim);
+          store8<P>(p + dim, B[i], i, dim);
+        }
+        if (RES) store8<P>(p + 2 * (long long)dim, C[i], i, dim);
+      }
+      continue;
+    }
+    float* p = a.part + (long long)blockIdx.x * 3 * dim;
+    auto add_up = [&](float* to, const float (&t)[8], int i) {       // columns of this thread alone
+      float s[8];
+      if (first) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = 0.f;
+      } else {
+        load8<P>(s, to, i, dim);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] += t[e];
+      store8<P>(to, s, i, dim);
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float t[8], w[8], b[8];
+      if (NORM) {
+        load_param<P>(w, a.weight, 0, a.param_bf16, 1.f, i, dim);
+        load_param<P>(b, a.bias, 0, a.param_bf16, 0.f, i, dim);
+        if (a.dshift) store8<P>(a.dshift + g * dim, A[i], i, dim);
+        if (a.dscale) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[e] = w[e] * B[i][e] + b[e] * A[i][e];
+          store8<P>(a.dscale + g * dim, t, i, dim);
+        }
+        if (weights) {
+          load_param<P>(b, a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[e] = (1.f + b[e]) * A[i][e];
+          add_up(p, t, i);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[e] = (1.f + b[e]) * B[i][e];
+          add_up(p + dim, t, i);
+        }
+      }
+      if (RES) {
+        load_param<P>(w, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
+        if (a.dgate) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[e] = a.residual_scale * w[e] * C[i][e];
+          store8<P>(a.dgate + g * dim, t, i, dim);
+        }
+        if (weights) {
+          load_param<P>(b, a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[e] = a.residual_scale * b[e] * C[i][e];
+          add_up(p + 2 * (long long)dim, t, i);
+        }
+      }
+    }
+    first = false;
+  }
+  if (RING) wait_async<0>();
+}
+
+// ----------------------------------------------------------------- launch --
+template <typename XT, typename BT, int P, bool RING, int NV, bool RES, bool NORM>
+cudaError_t run(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
+  constexpr int K = NV == 1 ? 2 : 1;
+  const int threads = row_threads(a.dim, NV);
+  const size_t slot = slot_bytes(threads, NV, sizeof(XT)) * (NORM ? 2 : 1) +
+                      slot_bytes(threads, NV, sizeof(BT)) * ((RES ? 1 : 0) + (NORM ? 1 : 0));
+  int depth = 0;
+  size_t smem = 0;
+  if (RING) {
+    const size_t room = kSmemSm / bwd_blocks(a.dim) - 1024 - sizeof(Shared<K>);
+    const long long rows = (a.rows + grid - 1) / grid;
+    depth = (int)(room / slot < kDepthMax ? room / slot : kDepthMax);
+    if (rows < depth) depth = (int)(rows > K ? rows : K);
+    if (depth < K) return cudaErrorInvalidConfiguration;
+    smem = depth * slot;
+  }
+  const auto kernel = row_bwd_kernel<XT, BT, P, RING, NV, K, RES, NORM>;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, threads, smem, s>>>(a, depth, weights);
+  return cudaGetLastError();
+}
+
+template <typename XT, typename BT, int P, bool RING, int NV>
+cudaError_t by_op(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
+  if (a.dy && a.dh) return run<XT, BT, P, RING, NV, true, true>(a, grid, weights, s);
+  if (a.dy) return run<XT, BT, P, RING, NV, true, false>(a, grid, weights, s);
+  return run<XT, BT, P, RING, NV, false, true>(a, grid, weights, s);
+}
+
+// Rows above 8192 elements are read where they are used.
+template <typename XT, typename BT, int P, bool RING>
+cudaError_t by_width(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
+  switch (row_nv(a.dim)) {
+    case 1: return by_op<XT, BT, P, RING, 1>(a, grid, weights, s);
+    case 2: return by_op<XT, BT, P, RING, 2>(a, grid, weights, s);
+    default: return by_op<XT, BT, P == 2 ? 1 : P, false, 4>(a, grid, weights, s);
+  }
+}
+
+}  // namespace
+
+template <typename XT, typename BT>
+cudaError_t row_bwd(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
+  const int p = piece_of(a);
+  if constexpr (sizeof(XT) == 2) {
+    if (p == 8) return by_width<XT, BT, 8, true>(a, grid, weights, s);
+    return p > 1 ? by_width<XT, BT, 2, true>(a, grid, weights, s) : by_width<XT, BT, 1, false>(a, grid, weights, s);
+  } else {
+    return p == 4 ? by_width<XT, BT, 4, true>(a, grid, weights, s)
+                  : by_width<XT, BT, 1, sizeof(BT) == 4>(a, grid, weights, s);
+  }
+}
+
+}  // namespace spade

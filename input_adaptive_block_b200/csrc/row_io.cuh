@@ -1,6 +1,7 @@
 // Row access and reductions shared by the row passes around the attention
-// (k_qk_rope.cu, k_row_norm.cu): eight-element loads and stores of float32 or
-// bfloat16 rows, and block-wide sums and moments in float32.
+// (k_qk_rope.cu, row_pass.cuh): loads, stores and asynchronous
+// copies of eight float32 or bfloat16 elements in pieces of P, and sums over
+// warps and blocks in float32.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -9,100 +10,178 @@
 namespace spade {
 namespace rowio {
 
-// Eight elements as they lie in memory: 16 bytes of bfloat16, 32 of float32.
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<__nv_bfloat16> {
-  uint4 u;
-};
-template <>
-struct Raw8<float> {
-  float4 a, b;
-};
+using bf16 = __nv_bfloat16;
 
-__device__ __forceinline__ void load_raw(Raw8<__nv_bfloat16>& r, const __nv_bfloat16* p) {
-  r.u = *reinterpret_cast<const uint4*>(p);
-}
-__device__ __forceinline__ void load_raw(Raw8<float>& r, const float* p) {
-  r.a = *reinterpret_cast<const float4*>(p);
-  r.b = *reinterpret_cast<const float4*>(p + 4);
-}
-__device__ __forceinline__ void clear_raw(Raw8<__nv_bfloat16>& r) { r.u = make_uint4(0u, 0u, 0u, 0u); }
-__device__ __forceinline__ void clear_raw(Raw8<float>& r) { r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f); }
+template <int BYTES>
+struct Word;
+template <> struct Word<2> { using type = unsigned short; };
+template <> struct Word<4> { using type = unsigned int; };
+template <> struct Word<8> { using type = uint2; };
+template <> struct Word<16> { using type = uint4; };
+struct alignas(16) Word32 { uint4 a, b; };
+template <> struct Word<32> { using type = Word32; };
 
-// bfloat16 is the upper half of a float32: the low element of a word shifts
-// up, the high one is masked.
-__device__ __forceinline__ void unpack(float (&v)[8], const Raw8<__nv_bfloat16>& r) {
-  const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+// P neighbouring elements as one access.  bfloat16 is the upper half of a
+// float32: the low element of a word shifts up, the high one is masked.
+template <int P>
+__device__ __forceinline__ void widen(float* v, const uint32_t* w, bf16) {
+  if (P == 1) {
+    v[0] = __uint_as_float(w[0] << 16);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < P / 2; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
 }
-__device__ __forceinline__ void unpack(float (&v)[8], const Raw8<float>& r) {
-  v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
-  v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+template <int P>
+__device__ __forceinline__ void widen(float* v, const uint32_t* w, float) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) v[i] = __uint_as_float(w[i]);
 }
+__device__ __forceinline__ void words_of(uint32_t* w, unsigned short u) { w[0] = u; }
+__device__ __forceinline__ void words_of(uint32_t* w, unsigned int u) { w[0] = u; }
+__device__ __forceinline__ void words_of(uint32_t* w, uint2 u) { w[0] = u.x; w[1] = u.y; }
+__device__ __forceinline__ void words_of(uint32_t* w, uint4 u) { w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w; }
+__device__ __forceinline__ void words_of(uint32_t* w, const Word32& u) { words_of(w, u.a); words_of(w + 4, u.b); }
+__device__ __forceinline__ void from_words(unsigned short& u, const uint32_t* w) { u = (unsigned short)w[0]; }
+__device__ __forceinline__ void from_words(unsigned int& u, const uint32_t* w) { u = w[0]; }
+__device__ __forceinline__ void from_words(uint2& u, const uint32_t* w) { u = make_uint2(w[0], w[1]); }
+__device__ __forceinline__ void from_words(uint4& u, const uint32_t* w) { u = make_uint4(w[0], w[1], w[2], w[3]); }
+__device__ __forceinline__ void from_words(Word32& u, const uint32_t* w) { from_words(u.a, w); from_words(u.b, w + 4); }
 
-__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[8]) {
-  uint4 u;
+template <typename T, int P>
+__device__ __forceinline__ void load_piece(float* v, const T* p) {
+  using W = typename Word<P * (int)sizeof(T)>::type;
+  uint32_t w[8];
+  words_of(w, *reinterpret_cast<const W*>(p));
+  widen<P>(v, w, T());
+}
+template <int P>
+__device__ __forceinline__ void store_piece(bf16* p, const float* v) {      // rounds to nearest even
   uint32_t w[4];
+  if (P == 1) {
+    w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < P / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
   }
-  u = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(p) = u;
+  typename Word<P * 2>::type u;
+  from_words(u, w);
+  *reinterpret_cast<typename Word<P * 2>::type*>(p) = u;
 }
-__device__ __forceinline__ void store_vec(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-__device__ __forceinline__ float warp_sum(float v) {
+template <int P>
+__device__ __forceinline__ void store_piece(float* p, const float* v) {
+  uint32_t w[8];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int i = 0; i < P; ++i) w[i] = __float_as_uint(v[i]);
+  typename Word<P * 4>::type u;
+  from_words(u, w);
+  *reinterpret_cast<typename Word<P * 4>::type*>(p) = u;
 }
 
-// Scratch of block_sum for up to M values at once, in two halves.
+// Asynchronous copy of 4, 8 or 16 bytes to shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "no such copy");
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else if (BYTES == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void commit_async() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_async() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Waits until at most `left` of this thread's groups are in flight (waits for
+// more than asked where `left` is above the cases).
+__device__ __forceinline__ void wait_async_upto(int left) {
+  switch (left) {
+    case 0: wait_async<0>(); break;
+    case 1: wait_async<1>(); break;
+    case 2: wait_async<2>(); break;
+    case 3: wait_async<3>(); break;
+    case 4: wait_async<4>(); break;
+    case 5: wait_async<5>(); break;
+    case 6: wait_async<6>(); break;
+    case 7: wait_async<7>(); break;
+    case 8: wait_async<8>(); break;
+    case 9: wait_async<9>(); break;
+    case 10: wait_async<10>(); break;
+    case 11: wait_async<11>(); break;
+    default: wait_async<12>(); break;
+  }
+}
+
+// Sums N values (a power of two, up to 32) over the warp at once: halves of
+// the values change places until every lane carries one, so N - 1 + 5 -
+// log2(N) shuffles do for all of them.  Lane l gets the sum of value
+// l / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sum_spread(const float (&in)[N]) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = in[i];
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int n = N; n > 1; n >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float give = up ? v[i] : v[i + n / 2], keep = up ? v[i + n / 2] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+    o >>= 1;
+  }
+  float s = v[0];
+#pragma unroll
+  for (; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+// Adds up the 32 / N lanes that share a value.
+template <int N>
+__device__ __forceinline__ float spread_sum(float s) {
+#pragma unroll
+  for (int o = 16 / N; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+// Every lane gets all N values.
+template <int N>
+__device__ __forceinline__ void spread_get(float (&v)[N], float s) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, s, i * (32 / N));
+}
+
+// Scratch of block-wide sums of up to M float2 values, in two halves.  Calls
+// on one scratch alternate its halves, whatever they sum, so one barrier a
+// call is enough: a half is written again only after the next call's barrier,
+// which every thread reaches after its reads of this one.
 template <int M>
-struct SumScratch {
-  float v[2][M * 32];
+struct Scratch {
+  float2 v[2][M * 33];
 };
 
-// Sums of K values over the block, the same in every thread.  Calls on one
-// scratch alternate its halves, whatever their K, so one barrier per call is
-// enough: a half is written again only after the next call's barrier, which
-// every thread reaches after its reads of this one.  One-warp blocks need no
-// barrier.
-template <int K, int M>
-__device__ __forceinline__ void block_sum(float (&v)[K], SumScratch<M>& buf, int& half, int nwarps) {
-  static_assert(K <= M, "scratch too small");
-#pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-  if (nwarps == 1) return;
-  float* b = buf.v[half];
-  if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) b[k * 32 + (threadIdx.x >> 5)] = v[k];
+// Sums of N values over the block, the same in every thread.  One barrier,
+// none in one-warp blocks.
+template <int N, int M>
+__device__ __forceinline__ void block_sum(float (&v)[N], Scratch<M>& sh, int& half, int nwarps) {
+  static_assert(N <= 2 * M, "scratch too small");
+  constexpr int L = 32 / N;
+  const int lane = threadIdx.x & 31, sub = lane % L;
+  float s = warp_sum_spread<N>(v);
+  if (nwarps > 1) {
+    float* b = reinterpret_cast<float*>(sh.v[half]) + (lane / L) * 33;
+    if (sub == 0) b[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.f;
+    for (int w = sub; w < nwarps; w += L) s += b[w];
+    s = spread_sum<N>(s);
+    half ^= 1;
   }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    float s = 0.f;
-    for (int w = 0; w < nwarps; ++w) s += b[k * 32 + w];
-    v[k] = s;
-  }
-  half ^= 1;
+  spread_get<N>(v, s);
 }
 
 }  // namespace rowio

@@ -1,0 +1,347 @@
+// What the forward and the backward row passes share: which columns a thread
+// owns, the ring of rows in shared memory, and the statistics of a row.
+//
+// A block holds K rows at a time and a thread the same columns of each: NV
+// times eight, in pieces of P neighbours that lie P * blockDim apart, so that a
+// warp's access is contiguous.  P is the widest piece that the row length and
+// every row's address allow (16 bytes; a single element in the worst case).
+// Rows that come in are copied ahead of their use into a ring of `depth` rows
+// (RING): every thread copies and reads its own columns only, so a ring needs
+// no barrier, and keeps some 100 KB in flight on an SM, which a load into
+// registers could not.  Without RING (pieces below 4 bytes, or rows of which
+// not two fit in shared memory) rows are read from global memory where they
+// are used.
+#pragma once
+#include "row_io.cuh"
+#include "spade_internal.cuh"
+
+namespace spade {
+namespace rowpass {
+
+using namespace rowio;
+
+enum { kNone = SPADE_NORM_NONE, kRms = SPADE_NORM_RMS, kLayer = SPADE_NORM_LAYER };
+
+template <int P>
+__device__ __forceinline__ int column(int i, int e) {
+  return ((i * (8 / P) + e / P) * (int)blockDim.x + (int)threadIdx.x) * P + e % P;
+}
+
+template <int P, typename T>
+__device__ __forceinline__ void load8(float (&v)[8], const T* row, int i, int dim) {
+#pragma unroll
+  for (int e = 0; e < 8; e += P) {
+    const int c = column<P>(i, e);
+    if (c < dim) {
+      load_piece<T, P>(v + e, row + c);
+    } else {
+#pragma unroll
+      for (int q = 0; q < P; ++q) v[e + q] = 0.f;
+    }
+  }
+}
+template <int P, typename T>
+__device__ __forceinline__ void store8(T* row, const float (&v)[8], int i, int dim) {
+#pragma unroll
+  for (int e = 0; e < 8; e += P) {
+    const int c = column<P>(i, e);
+    if (c < dim) store_piece<P>(row + c, v + e);
+  }
+}
+// A parameter row in either type; absent ones read as `none`.
+template <int P>
+__device__ __forceinline__ void load_param(float (&v)[8], const void* p, long long off, bool is_bf16, float none, int i,
+                                           int dim) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = none;
+  } else if (is_bf16) {
+    load8<P>(v, static_cast<const bf16*>(p) + off, i, dim);
+  } else {
+    load8<P>(v, static_cast<const float*>(p) + off, i, dim);
+  }
+}
+
+// One operand of the ring: its place in a slot, and where its rows come from.
+template <typename T, int P, bool RING, int NV>
+struct Stream {
+  const T* base;
+  long long stride;
+  uint32_t at;       // bytes into a slot
+
+  __device__ __forceinline__ void fetch(uint32_t slot, long long r, int dim) const {
+    if constexpr (RING) {
+      const T* row = base + r * stride;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; e += P) {
+          const int c = column<P>(i, e);
+          if (c < dim) copy_async<P * (int)sizeof(T)>(slot + at + c * (int)sizeof(T), row + c);
+        }
+    }
+  }
+  // Columns past the row's end read as zero.
+  __device__ __forceinline__ void clear(unsigned char* slot, int dim) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = column<P>(i, e);
+        if (c >= dim) reinterpret_cast<T*>(slot + at)[c] = T(0.f);
+      }
+  }
+  __device__ __forceinline__ void get(float (&v)[8], const unsigned char* slot, long long r, int i, int dim) const {
+    if constexpr (RING) {
+      const T* row = reinterpret_cast<const T*>(slot + at);
+#pragma unroll
+      for (int e = 0; e < 8; e += P) load_piece<T, P>(v + e, row + column<P>(i, e));
+    } else {
+      load8<P>(v, base + r * stride, i, dim);
+    }
+  }
+};
+
+// The bytes an operand takes in a slot.
+__host__ __device__ inline uint32_t slot_bytes(int threads, int nv, int elem) { return (uint32_t)(threads * nv * 8 * elem); }
+
+template <int K>
+struct Shared {
+  Scratch<2 * K> sums;
+  float count[32];     // columns each warp owns
+};
+
+template <int P, int NV>
+__device__ __forceinline__ void count_columns(float* count, int dim) {
+  float c[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[0] += column<P>(i, e) < dim ? 1.f : 0.f;
+  const float s = warp_sum_spread<1>(c);
+  if ((threadIdx.x & 31) == 0) count[threadIdx.x >> 5] = s;
+  __syncthreads();
+}
+
+// Mean (0 for the rms norm) and reciprocal deviation of K rows held in
+// registers.  The layer norm's second moment is taken about each warp's own
+// mean and the warps' moments are merged (Chan, Golub and LeVeque, 1979), so
+// a row far from zero loses nothing and one barrier is enough.
+template <int P, int NV, int K>
+__device__ __forceinline__ void row_stats(const float (&v)[K][NV][8], int kind, float eps, int dim, Shared<K>& sh,
+                                          int& half, int nwarps, float (&mean)[K], float (&rstd)[K]) {
+  const float inv_dim = 1.f / (float)dim;
+  float s[K];
+  if (kind == kRms) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      s[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[k] += v[k][i][e] * v[k][i][e];
+    }
+    block_sum(s, sh.sums, half, nwarps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      mean[k] = 0.f;
+      rstd[k] = rsqrtf(s[k] * inv_dim + eps);
+    }
+    return;
+  }
+  constexpr int L = 32 / K, W = (32 + L - 1) / L;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
+  const float n = sh.count[warp];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    s[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[k] += v[k][i][e];
+  }
+  const float own = n > 0.f ? warp_sum_spread<K>(s) / n : 0.f;      // of the row this lane stands for
+  float m[K];
+  spread_get<K>(m, own);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    s[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = column<P>(i, e) < dim ? v[k][i][e] - m[k] : 0.f;
+        s[k] += t * t;
+      }
+  }
+  float q = warp_sum_spread<K>(s);
+  float mu = own;
+  if (nwarps > 1) {
+    float2* b = sh.sums.v[half] + (lane / L) * 33;
+    if (sub == 0) b[warp] = make_float2(own, q);
+    __syncthreads();
+    float2 p[W];
+    float total = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const int w = sub + j * L;
+      p[j] = w < nwarps ? b[w] : make_float2(0.f, 0.f);
+      if (w < nwarps) total += sh.count[w] * p[j].x;
+    }
+    mu = spread_sum<K>(total) * inv_dim;
+    q = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const int w = sub + j * L;
+      if (w < nwarps) q += p[j].y + sh.count[w] * (p[j].x - mu) * (p[j].x - mu);
+    }
+    q = spread_sum<K>(q);
+    half ^= 1;
+  }
+  spread_get<K>(mean, mu);
+  spread_get<K>(rstd, rsqrtf(q * inv_dim + eps));
+}
+
+// The statistics of K rows x' and, for the gradient u that reaches their norm,
+// mean(u) (0 for the rms norm) and mean(u xhat), with one barrier: the sums
+// with u are taken about the warps' means as well and merged alike.
+template <int P, int NV, int K>
+__device__ __forceinline__ void row_stats_bwd(const float (&v)[K][NV][8], const float (&u)[K][NV][8], int kind, float eps,
+                                              int dim, Shared<K>& sh, int& half, int nwarps, float (&mean)[K],
+                                              float (&rstd)[K], float (&mu0)[K], float (&mu1)[K]) {
+  const float inv_dim = 1.f / (float)dim;
+  float s[2 * K];
+  if (kind == kRms) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      s[k] = s[K + k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s[k] += v[k][i][e] * v[k][i][e];
+          s[K + k] += u[k][i][e] * v[k][i][e];
+        }
+    }
+    block_sum(s, sh.sums, half, nwarps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      mean[k] = mu0[k] = 0.f;
+      rstd[k] = rsqrtf(s[k] * inv_dim + eps);
+      mu1[k] = s[K + k] * inv_dim * rstd[k];
+    }
+    return;
+  }
+  // values of a warp: first the sums of x' and u, then the second moment and
+  // the sum of u (x' - its mean)
+  constexpr int N = 2 * K, L = 32 / N, W = (32 + L - 1) / L;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
+  const float n = sh.count[warp], inv_n = n > 0.f ? 1.f / n : 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    s[k] = s[K + k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s[k] += v[k][i][e];
+        s[K + k] += u[k][i][e];
+      }
+  }
+  float first = warp_sum_spread<N>(s);
+  if (lane < 16) first *= inv_n;                 // lanes below 16 stand for x', the others for u
+  float m[N];
+  spread_get<N>(m, first);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    s[k] = s[K + k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = column<P>(i, e) < dim ? v[k][i][e] - m[k] : 0.f;
+        s[k] += t * t;
+        s[K + k] += u[k][i][e] * t;
+      }
+  }
+  float second = warp_sum_spread<N>(s);
+  float mu = first;
+  if (nwarps > 1) {
+    float2* b = sh.sums.v[half] + (lane / L) * 33;
+    if (sub == 0) b[warp] = make_float2(first, second);
+    __syncthreads();
+    const float2* bx = sh.sums.v[half] + ((lane & 15) / L) * 33;     // x' of the row this lane stands for
+    float2 p[W];
+    float xm[W];
+    float total = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const int w = sub + j * L;
+      p[j] = w < nwarps ? b[w] : make_float2(0.f, 0.f);
+      xm[j] = w < nwarps ? bx[w].x : 0.f;
+      if (w < nwarps) total += lane < 16 ? sh.count[w] * p[j].x : p[j].x;
+    }
+    mu = spread_sum<N>(total);
+    if (lane < 16) mu *= inv_dim;
+    const float mx = __shfl_sync(0xffffffffu, mu, lane & 15);
+    second = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const int w = sub + j * L;
+      const float off = xm[j] - mx;
+      if (w < nwarps) second += p[j].y + off * (lane < 16 ? sh.count[w] * off : p[j].x);
+    }
+    second = spread_sum<N>(second);
+    half ^= 1;
+  }
+  if (lane < 16) second = rsqrtf(second * inv_dim + eps);
+  float a[N], b2[N];
+  spread_get<N>(a, mu);
+  spread_get<N>(b2, second);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    mean[k] = a[k];
+    rstd[k] = b2[k];
+    mu0[k] = a[K + k] * inv_dim;
+    mu1[k] = b2[K + k] * inv_dim * b2[k];
+  }
+}
+
+// ----------------------------------------------------------------- launch --
+// The widest piece, in elements, that every row of every operand allows.
+inline int piece_of(const RowArgs& a) {
+  const int ex = a.x_bf16 ? 2 : 4, eb = a.branch_bf16 ? 2 : 4, ep = a.param_bf16 ? 2 : 4;
+  const struct { const void* p; long long stride; int size; } ops[] = {
+      {a.x, a.x_stride, ex}, {a.x_out, a.x_out_stride, ex}, {a.dx_out, a.dx_out_stride, ex}, {a.dx, a.dx_stride, ex},
+      {a.y, a.y_stride, eb}, {a.h, a.h_stride, eb}, {a.dh, a.dh_stride, eb}, {a.dy, a.dy_stride, eb},
+      {a.gate, a.gate_stride, ep}, {a.scale, a.scale_stride, ep}, {a.shift, a.shift_stride, ep}, {a.weight, 0, ep},
+      {a.bias, 0, ep}, {a.post_weight, 0, ep}, {a.dgate, a.dim, 4}, {a.dscale, a.dim, 4}, {a.dshift, a.dim, 4}};
+  for (int p = ex == 2 && eb == 2 ? 8 : 4; p > 1; p >>= 1) {
+    bool ok = a.dim % p == 0;
+    for (const auto& o : ops) {
+      const int need = p * o.size < 16 ? p * o.size : 16;
+      ok = ok && (!o.p || (reinterpret_cast<uintptr_t>(o.p) % need == 0 && o.stride % p == 0));
+    }
+    if (ok) return p;
+  }
+  return 1;
+}
+
+constexpr int kSmemSm = 227 * 1024;     // shared memory of an SM that blocks can use
+constexpr int kDepthMax = 14;           // rows of a ring: wait_async_upto covers depth - K
+
+inline int row_threads(int dim, int nv) {
+  const int t = (dim + 8 * nv - 1) / (8 * nv);
+  return (t + 31) / 32 * 32;
+}
+inline int row_nv(int dim) { return dim <= 5120 ? 1 : (dim <= 8192 ? 2 : 4); }
+
+// Blocks of an SM, by registers (96 a thread; 128 of the wide rows').
+inline int bwd_blocks(int dim) {
+  const int threads = row_threads(dim, row_nv(dim));
+  const int b = row_nv(dim) > 1 ? 1 : 640 / threads;
+  return b < 1 ? 1 : (b > 16 ? 16 : b);
+}
+
+}  // namespace rowpass
+}  // namespace spade

@@ -706,6 +706,7 @@ spade_status run_row_bwd(const spade_row_desc* desc, const spade_row_params* par
   if (!res && (a.dgate || a.dpost_weight)) return fail(SPADE_ERR_INVALID, "gradients of gate parameters without a residual");
   if (a.dpost_weight && a.post_norm == SPADE_NORM_NONE)
     return fail(SPADE_ERR_INVALID, "gradient of post_weight without a post_norm");
+  if (a.rows && res && norm && dx == y) return fail(SPADE_ERR_INVALID, "dx overlaps y");   // y is read again after dx
   Regions rs;
   add_params(rs, a);
   const struct { const char* name; float* p; long long len; } gs[] = {

@@ -105,7 +105,7 @@ size_t sics_workspace_floats(const Geo* cand, int n_cand, int heads);
 cudaError_t launch_sics(const void* q, const void* k, const Geo* cand, int n_cand, int heads, int d, spade_dtype dt,
                         float* ws, float* scores, int* choice, cudaStream_t s);
 
-// One row pass of the residual stream (k_row_norm.cu).  Null pointers: no
+// One row pass of the residual stream (k_row.cu).  Null pointers: no
 // such operand (parameters: the identity); strides in elements.
 struct RowArgs {
   long long rows, groups, rows_per_group, chunks;

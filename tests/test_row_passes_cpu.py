@@ -238,6 +238,7 @@ def test_row_refusals():
     assert _row(bwd, g={"gate": W}, ws=BASE) == SPADE_ERR_INVALID
     assert _row(bwd, g={"gate": W + 2}) == SPADE_ERR_INVALID
     assert _row(bwd, p={"gate": W}, g={"gate": W}) == SPADE_ERR_INVALID            # a gradient over its parameter
+    assert _row(bwd, branch_dt=0, ptrs={"d": 2 * BASE}) == SPADE_ERR_INVALID       # dx over y, which is read later
     assert _row(bwd, g={"gate": W, "shift": W + 1024}) == SPADE_ERR_INVALID
     assert _row(bwd, g={"post_weight": W}) == SPADE_ERR_INVALID
     assert _row("norm_modulate_bwd", g={"gate": W}) == SPADE_ERR_INVALID
