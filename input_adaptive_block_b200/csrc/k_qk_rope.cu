@@ -45,23 +45,43 @@ template <int P, bool HALF>
 __device__ __forceinline__ bool owned(int j, int lanes, int e, int d) {
   return HALF ? channel<P, HALF>(j, lanes, e & 7, d) < (d >> 1) : channel<P, HALF>(j, lanes, e, d) < d;
 }
-// Where the angle of pair p lies: as entry m of lane j, so that a thread reads
-// its eight as four 16-byte words, without bank conflicts.
+// Where the cosine of pair p lies, its sine two floats on: as entry m of lane
+// j, two entries to a 16-byte word (cos, cos, sin, sin), so that a thread reads
+// its eight as four words, without bank conflicts, ready for paired arithmetic.
 template <int P, bool HALF>
 __device__ __forceinline__ int angle_slot(int p, int lanes) {
   constexpr int O = !HALF && P == 1 ? 2 : P;
   const int c = HALF ? p : 2 * p, piece = c / O;
   const int e = piece / lanes * O + c % O, j = piece & (lanes - 1), m = HALF ? e : e >> 1;
-  return ((m >> 1) * lanes + j) * 2 + (m & 1);
+  return ((m >> 1) * lanes + j) * 4 + (m & 1);
+}
+
+// A thread's unit: its sixteen elements in global memory and in the ring, and
+// as eight rotated pairs (a, b), two and two together.
+struct Unit {
+  float2 a[4], b[4];
+};
+template <bool HALF>
+__device__ __forceinline__ void pairs_of(Unit& u, const float (&v)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    u.a[q] = HALF ? make_float2(v[2 * q], v[2 * q + 1]) : make_float2(v[4 * q], v[4 * q + 2]);
+    u.b[q] = HALF ? make_float2(v[2 * q + 8], v[2 * q + 9]) : make_float2(v[4 * q + 1], v[4 * q + 3]);
+  }
 }
 template <bool HALF>
-__device__ __forceinline__ constexpr int first_of(int m) { return HALF ? m : 2 * m; }
-template <bool HALF>
-__device__ __forceinline__ constexpr int second_of(int m) { return HALF ? m + 8 : 2 * m + 1; }
-
-// A thread's unit: its sixteen elements in global memory and in the ring.
+__device__ __forceinline__ void elements_of(float (&v)[16], const Unit& u) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    v[HALF ? 2 * q : 4 * q] = u.a[q].x;
+    v[HALF ? 2 * q + 1 : 4 * q + 2] = u.a[q].y;
+    v[HALF ? 2 * q + 8 : 4 * q + 1] = u.b[q].x;
+    v[HALF ? 2 * q + 9 : 4 * q + 3] = u.b[q].y;
+  }
+}
 template <typename T, int P, bool HALF>
-__device__ __forceinline__ void load16(float (&v)[16], const T* head, bool in, int j, int lanes, int d) {
+__device__ __forceinline__ void load16(Unit& u, const T* head, bool in, int j, int lanes, int d) {
+  float v[16];
 #pragma unroll
   for (int e = 0; e < 16; e += P) {
     if (in && owned<P, HALF>(j, lanes, e, d)) {
@@ -71,9 +91,12 @@ __device__ __forceinline__ void load16(float (&v)[16], const T* head, bool in, i
       for (int q = 0; q < P; ++q) v[e + q] = 0.f;
     }
   }
+  pairs_of<HALF>(u, v);
 }
 template <typename T, int P, bool HALF>
-__device__ __forceinline__ void store16(T* head, const float (&v)[16], int j, int lanes, int d) {
+__device__ __forceinline__ void store16(T* head, const Unit& u, int j, int lanes, int d) {
+  float v[16];
+  elements_of<HALF>(v, u);
 #pragma unroll
   for (int e = 0; e < 16; e += P)
     if (owned<P, HALF>(j, lanes, e, d)) store_piece<P>(head + channel<P, HALF>(j, lanes, e, d), v + e);
@@ -87,11 +110,13 @@ __device__ __forceinline__ void fetch16(uint32_t to, const T* head, int j, int l
       copy_async<P * (int)sizeof(T)>(to + (e / P * blockDim.x + threadIdx.x) * P * (int)sizeof(T),
                                      head + channel<P, HALF>(j, lanes, e, d));
 }
-template <typename T, int P>
-__device__ __forceinline__ void ring16(float (&v)[16], const unsigned char* at) {
+template <typename T, int P, bool HALF>
+__device__ __forceinline__ void ring16(Unit& u, const unsigned char* at) {
   const T* p = reinterpret_cast<const T*>(at);
+  float v[16];
 #pragma unroll
   for (int e = 0; e < 16; e += P) load_piece<T, P>(v + e, p + (e / P * blockDim.x + threadIdx.x) * P);
+  pairs_of<HALF>(u, v);
 }
 // What is not copied reads as zero.
 template <typename T, int P, bool HALF>
@@ -107,36 +132,54 @@ struct Turns {
   int axis[SPADE_ROPE_MAX_PAIRS];
 };
 
+// n / divisor for n below 2^31 (Granlund and Montgomery, 1994).
+__device__ __forceinline__ unsigned divide(unsigned n, const QkArgs::Divisor& by) {
+  return (unsigned)(((unsigned long long)n * by.mul) >> by.shift);
+}
+
 // Cosine and sine of every pair of the block's next tokens.
 template <int P, bool HALF, int K>
-__device__ __forceinline__ void angles(const QkArgs& a, const Turns& tu, long long r0, long long r1, float2* cs) {
+__device__ __forceinline__ void angles(const QkArgs& a, const Turns& tu, long long r0, long long r1, float* cs) {
   const int half_d = a.d >> 1;
   for (int i = threadIdx.x; i < K * half_d; i += blockDim.x) {
-    const int k = i / half_d, p = i - k * half_d;
+    const int k = K == 2 && i >= half_d ? 1 : 0, p = i - k * half_d;
     const long long r = r0 + k;
-    float2 v = make_float2(1.f, 0.f);
+    float c = 1.f, s = 0.f;
     if (p < a.pairs && r < a.video_rows && r < r1) {
       const int axis = tu.axis[p];
       int pos;
       if (a.positions) {
         pos = a.positions[r * 3 + axis];
       } else {
-        const unsigned tok = (unsigned)a.tok0 + (unsigned)r, row = tok / (unsigned)a.W;
-        pos = axis == 2 ? tok - row * (unsigned)a.W
-                        : (axis == 1 ? row % (unsigned)a.H : row / (unsigned)a.H);
+        const unsigned tok = (unsigned)a.tok0 + (unsigned)r, row = divide(tok, a.W), t = divide(row, a.H);
+        pos = axis == 2 ? tok - row * a.W.by : (axis == 1 ? row - t * a.H.by : t);
       }
       const double t = (double)pos * tu.turn[p];
-      sincospif(2.f * (float)(t - rint(t)), &v.y, &v.x);
+      sincospif(2.f * (float)(t - rint(t)), &s, &c);
     }
-    cs[k * 8 * a.lanes + angle_slot<P, HALF>(p, a.lanes)] = v;
+    float* o = cs + k * 16 * a.lanes + angle_slot<P, HALF>(p, a.lanes);
+    o[0] = c;
+    o[2] = s;
   }
 }
-__device__ __forceinline__ void get_angles(float2 (&c)[8], const float2* cs, int j, int lanes) {
+struct Angles {
+  float2 c[4], s[4];
+};
+__device__ __forceinline__ void get_angles(Angles& t, const float* cs, int j, int lanes) {
 #pragma unroll
-  for (int m = 0; m < 8; m += 2) {
-    const float4 f = *reinterpret_cast<const float4*>(cs + (m * lanes + j * 2));
-    c[m] = make_float2(f.x, f.y);
-    c[m + 1] = make_float2(f.z, f.w);
+  for (int q = 0; q < 4; ++q) {
+    const float4 f = *reinterpret_cast<const float4*>(cs + (q * lanes + j) * 4);
+    t.c[q] = make_float2(f.x, f.y);
+    t.s[q] = make_float2(f.z, f.w);
+  }
+}
+// (a, b) -> (a c - b s, a s + b c), or back.
+__device__ __forceinline__ void turn(Unit& u, const Angles& t, bool back) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float2 minus = make_float2(-t.s[q].x, -t.s[q].y), a = u.a[q], b = u.b[q];
+    u.a[q] = fma(b, back ? t.s[q] : minus, mul(a, t.c[q]));
+    u.b[q] = fma(a, back ? minus : t.s[q], mul(b, t.c[q]));
   }
 }
 
@@ -161,9 +204,13 @@ struct Units {
     }
     slot = (uint32_t)(ops * UPT * 16 * sizeof(T)) * blockDim.x;
   }
+  // Unit i's head of row r, and the way to its next row.
   template <typename V>
   __device__ __forceinline__ V* at(V* const (&base)[2], const long long (&stride)[2], long long r, int i) const {
     return (k_side[i] ? base[1] + r * stride[1] : base[0] + r * stride[0]) + head[i] * d;
+  }
+  __device__ __forceinline__ long long step(const long long (&stride)[2], int i) const {
+    return k_side[i] ? stride[1] : stride[0];
   }
   __device__ __forceinline__ uint32_t place(int op, int i) const {
     return (uint32_t)((op * UPT + i) * 16 * sizeof(T)) * blockDim.x;
@@ -174,12 +221,12 @@ struct Units {
 #pragma unroll
         for (int i = 0; i < UPT; ++i) clear16<T, P, HALF>(ring + s * slot + place(o, i), in[i], j, lanes, d);
   }
-  __device__ __forceinline__ void weights(float (&w)[16], const QkArgs& a, int i) const {
+  __device__ __forceinline__ void weights(Unit& w, const QkArgs& a, int i) const {
     const void* p = a.weight[k_side[i]];
     const int off = a.norm == SPADE_QK_NORM_TOKEN ? head[i] * d : 0;
     if (!p || !in[i]) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) w[e] = 1.f;
+      for (int q = 0; q < 4; ++q) w.a[q] = w.b[q] = both(1.f);
     } else if (a.weight_bf16) {
       load16<bf16, P, HALF>(w, static_cast<const bf16*>(p) + off, true, j, lanes, d);
     } else {
@@ -192,12 +239,12 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ void read_turns(Turns& tu, const QkArgs& a, float2* cs, int n) {
+__device__ __forceinline__ void read_turns(Turns& tu, const QkArgs& a, float* cs, int n) {
   for (int i = threadIdx.x; i < a.pairs; i += blockDim.x) {
     tu.turn[i] = a.turn[i];
     tu.axis[i] = a.axis[i];
   }
-  for (int i = threadIdx.x; i < n; i += blockDim.x) cs[i] = make_float2(1.f, 0.f);    // pairs that heads lack
+  for (int i = threadIdx.x; i < n; i += blockDim.x) cs[i] = i & 2 ? 0.f : 1.f;    // pairs that heads lack
   __syncthreads();
 }
 
@@ -207,13 +254,20 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Turns tu;
   __shared__ Scratch<K> sums;
-  __shared__ __align__(16) float2 cs[2][K * SPADE_ROPE_MAX_PAIRS];
+  __shared__ __align__(16) float cs[2][K * 2 * SPADE_ROPE_MAX_PAIRS];
   const Units<T, P, HALF, RING, UPT> un(a, 1);
   const int lanes = un.lanes, j = un.j, d = un.d, nwarps = blockDim.x >> 5;
   const long long r0 = a.rows * blockIdx.x / gridDim.x, r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
   const T* const xs[2] = {static_cast<const T*>(a.x[0]), static_cast<const T*>(a.x[1])};
   T* const outs[2] = {static_cast<T*>(a.out[0]), static_cast<T*>(a.out[1])};
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  const T* from[UPT];            // the next token to copy and the next to write
+  T* to[UPT];
+#pragma unroll
+  for (int i = 0; i < UPT; ++i) {
+    from[i] = un.at(xs, a.x_stride, r0, i);
+    to[i] = un.at(outs, a.out_stride, r0, i);
+  }
   long long fr = r0;             // the next token to copy, its slot, and the slot of the next one to use
   int fs = 0, us = 0;
   auto fetch = [&]() {
@@ -221,7 +275,10 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
 #pragma unroll
       for (int i = 0; i < UPT; ++i)
         if constexpr (RING)
-          if (un.in[i]) fetch16<T, P, HALF>(ring_at + fs * un.slot + un.place(0, i), un.at(xs, a.x_stride, fr, i), j, lanes, d);
+          if (un.in[i]) {
+            fetch16<T, P, HALF>(ring_at + fs * un.slot + un.place(0, i), from[i], j, lanes, d);
+            from[i] += un.step(a.x_stride, i);
+          }
     }
     commit_async();
     ++fr;
@@ -231,17 +288,17 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
     un.clear(ring, depth, 1);
     for (int s = 0; s < depth; ++s) fetch();
   }
-  float w[UPT][16];
+  Unit w[UPT];
   const bool normed = a.norm != SPADE_QK_NORM_NONE, token = a.norm == SPADE_QK_NORM_TOKEN;
   if (normed) {
 #pragma unroll
     for (int i = 0; i < UPT; ++i) un.weights(w[i], a, i);
   }
-  read_turns(tu, a, cs[0], 2 * K * SPADE_ROPE_MAX_PAIRS);
+  read_turns(tu, a, cs[0], 4 * K * SPADE_ROPE_MAX_PAIRS);
   angles<P, HALF, K>(a, tu, r0, r1, cs[0]);
   int half = 0, buf = 0;
-  auto get = [&](float (&v)[16], const unsigned char* at, long long r, int i) {
-    if constexpr (RING) ring16<T, P>(v, at + un.place(0, i));
+  auto get = [&](Unit& v, const unsigned char* at, long long r, int i) {
+    if constexpr (RING) ring16<T, P, HALF>(v, at + un.place(0, i));
     else load16<T, P, HALF>(v, un.at(xs, a.x_stride, r, i), un.in[i], j, lanes, d);
   };
   for (long long r = r0; r < r1; r += K) {
@@ -257,11 +314,14 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
         s[k] = s[K + k] = 0.f;
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-          float v[16], q = 0.f;
+          float q = 0.f;
           if (k < n) {
+            Unit v;
+            float2 q2 = both(0.f);
             get(v, at[k], r + k, i);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) q += v[e] * v[e];
+            for (int p = 0; p < 4; ++p) q2 = fma(v.b[p], v.b[p], fma(v.a[p], v.a[p], q2));
+            q = sum_of(q2);
           }
           if (un.k_side[i]) s[K + k] += q;
           else s[k] += q;
@@ -285,24 +345,24 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (k >= n) break;
-      float2 c[8];
-      get_angles(c, cs[buf] + k * 8 * lanes, j, lanes);
+      Angles t;
+      get_angles(t, cs[buf] + k * 16 * lanes, j, lanes);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         if (!un.in[i]) continue;
-        float v[16];
+        Unit v;
         get(v, at[k], r + k, i);
         if (normed) {
+          const float2 f = both(rs[k][i]);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] *= rs[k][i] * w[i][e];
+          for (int p = 0; p < 4; ++p) {
+            v.a[p] = mul(v.a[p], mul(f, w[i].a[p]));
+            v.b[p] = mul(v.b[p], mul(f, w[i].b[p]));
+          }
         }
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          const float p0 = v[first_of<HALF>(m)], p1 = v[second_of<HALF>(m)];
-          v[first_of<HALF>(m)] = p0 * c[m].x - p1 * c[m].y;
-          v[second_of<HALF>(m)] = p0 * c[m].y + p1 * c[m].x;
-        }
-        store16<T, P, HALF>(un.at(outs, a.out_stride, r + k, i), v, j, lanes, d);
+        turn(v, t, false);
+        store16<T, P, HALF>(to[i], v, j, lanes, d);
+        to[i] += un.step(a.out_stride, i);
       }
     }
     if (RING) {
@@ -321,7 +381,7 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Turns tu;
   __shared__ Scratch<2 * K> sums;
-  __shared__ __align__(16) float2 cs[2][K * SPADE_ROPE_MAX_PAIRS];
+  __shared__ __align__(16) float cs[2][K * 2 * SPADE_ROPE_MAX_PAIRS];
   const bool normed = a.norm != SPADE_QK_NORM_NONE, token = a.norm == SPADE_QK_NORM_TOKEN;
   const int ops = normed ? 2 : 1;
   const Units<T, P, HALF, RING, UPT> un(a, ops);
@@ -331,6 +391,14 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
   const T* const xs[2] = {static_cast<const T*>(a.x[0]), static_cast<const T*>(a.x[1])};
   T* const outs[2] = {static_cast<T*>(a.out[0]), static_cast<T*>(a.out[1])};
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  const T *from_g[UPT], *from_x[UPT];     // the next token to copy and the next to write
+  T* to[UPT];
+#pragma unroll
+  for (int i = 0; i < UPT; ++i) {
+    from_g[i] = un.at(gs, a.dout_stride, r0, i);
+    from_x[i] = un.at(xs, a.x_stride, r0, i);
+    to[i] = un.at(outs, a.out_stride, r0, i);
+  }
   long long fr = r0;
   int fs = 0, us = 0;
   auto fetch = [&]() {
@@ -339,9 +407,13 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
       for (int i = 0; i < UPT; ++i)
         if constexpr (RING)
           if (un.in[i]) {
-            const uint32_t to = ring_at + fs * un.slot;
-            fetch16<T, P, HALF>(to + un.place(0, i), un.at(gs, a.dout_stride, fr, i), j, lanes, d);
-            if (normed) fetch16<T, P, HALF>(to + un.place(1, i), un.at(xs, a.x_stride, fr, i), j, lanes, d);
+            const uint32_t slot = ring_at + fs * un.slot;
+            fetch16<T, P, HALF>(slot + un.place(0, i), from_g[i], j, lanes, d);
+            from_g[i] += un.step(a.dout_stride, i);
+            if (normed) {
+              fetch16<T, P, HALF>(slot + un.place(1, i), from_x[i], j, lanes, d);
+              from_x[i] += un.step(a.x_stride, i);
+            }
           }
     }
     commit_async();
@@ -352,28 +424,23 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
     un.clear(ring, depth, ops);
     for (int s = 0; s < depth; ++s) fetch();
   }
-  float w[UPT][16], dw[UPT][16];
+  Unit w[UPT], dw[UPT];
 #pragma unroll
   for (int i = 0; i < UPT; ++i) {
     if (normed) un.weights(w[i], a, i);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) dw[i][e] = 0.f;
+    for (int p = 0; p < 4; ++p) dw[i].a[p] = dw[i].b[p] = both(0.f);
   }
-  read_turns(tu, a, cs[0], 2 * K * SPADE_ROPE_MAX_PAIRS);
+  read_turns(tu, a, cs[0], 4 * K * SPADE_ROPE_MAX_PAIRS);
   angles<P, HALF, K>(a, tu, r0, r1, cs[0]);
   int half = 0, buf = 0;
-  auto get_g = [&](float (&v)[16], const unsigned char* at, long long r, int i, const float2 (&c)[8]) {
-    if constexpr (RING) ring16<T, P>(v, at + un.place(0, i));
+  auto get_g = [&](Unit& v, const unsigned char* at, long long r, int i, const Angles& t) {
+    if constexpr (RING) ring16<T, P, HALF>(v, at + un.place(0, i));
     else load16<T, P, HALF>(v, un.at(gs, a.dout_stride, r, i), un.in[i], j, lanes, d);
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const float p0 = v[first_of<HALF>(m)], p1 = v[second_of<HALF>(m)];
-      v[first_of<HALF>(m)] = p0 * c[m].x + p1 * c[m].y;
-      v[second_of<HALF>(m)] = p1 * c[m].x - p0 * c[m].y;
-    }
+    turn(v, t, true);
   };
-  auto get_x = [&](float (&v)[16], const unsigned char* at, long long r, int i) {
-    if constexpr (RING) ring16<T, P>(v, at + un.place(1, i));
+  auto get_x = [&](Unit& v, const unsigned char* at, long long r, int i) {
+    if constexpr (RING) ring16<T, P, HALF>(v, at + un.place(1, i));
     else load16<T, P, HALF>(v, un.at(xs, a.x_stride, r, i), un.in[i], j, lanes, d);
   };
   for (long long r = r0; r < r1; r += K) {
@@ -390,20 +457,23 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
       for (int i = 0; i < 4 * K; ++i) s[i] = 0.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        float2 c[8];
-        get_angles(c, cs[buf] + k * 8 * lanes, j, lanes);
+        Angles t;
+        get_angles(t, cs[buf] + k * 16 * lanes, j, lanes);
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
           float q0 = 0.f, q1 = 0.f;
           if (k < n) {
-            float x[16], u[16];
+            Unit x, u;
+            float2 s0 = both(0.f), s1 = both(0.f);
             get_x(x, at[k], r + k, i);
-            get_g(u, at[k], r + k, i, c);
+            get_g(u, at[k], r + k, i, t);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              q0 += x[e] * x[e];
-              q1 += (u[e] * w[i][e]) * x[e];
+            for (int p = 0; p < 4; ++p) {
+              s0 = fma(x.b[p], x.b[p], fma(x.a[p], x.a[p], s0));
+              s1 = fma(mul(u.b[p], w[i].b[p]), x.b[p], fma(mul(u.a[p], w[i].a[p]), x.a[p], s1));
             }
+            q0 = sum_of(s0);
+            q1 = sum_of(s1);
           }
           if (un.k_side[i]) {
             s[K + k] += q0;
@@ -432,23 +502,27 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (k >= n) break;
-      float2 c[8];
-      get_angles(c, cs[buf] + k * 8 * lanes, j, lanes);
+      Angles t;
+      get_angles(t, cs[buf] + k * 16 * lanes, j, lanes);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         if (!un.in[i]) continue;                 // absent heads stay out of dw whatever eps makes of their zeros
-        float u[16];
-        get_g(u, at[k], r + k, i, c);
+        Unit u;
+        get_g(u, at[k], r + k, i, t);
         if (normed) {
-          float x[16];
+          Unit x;
           get_x(x, at[k], r + k, i);
+          const float2 f = both(rs[k][i]), g = both(-cf[k][i]);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            dw[i][e] += u[e] * (x[e] * rs[k][i]);
-            u[e] = rs[k][i] * (u[e] * w[i][e] - x[e] * cf[k][i]);
+          for (int p = 0; p < 4; ++p) {
+            dw[i].a[p] = fma(u.a[p], mul(x.a[p], f), dw[i].a[p]);
+            dw[i].b[p] = fma(u.b[p], mul(x.b[p], f), dw[i].b[p]);
+            u.a[p] = mul(f, fma(x.a[p], g, mul(u.a[p], w[i].a[p])));
+            u.b[p] = mul(f, fma(x.b[p], g, mul(u.b[p], w[i].b[p])));
           }
         }
-        store16<T, P, HALF>(un.at(outs, a.out_stride, r + k, i), u, j, lanes, d);
+        store16<T, P, HALF>(to[i], u, j, lanes, d);
+        to[i] += un.step(a.out_stride, i);
       }
     }
     if (RING) {
@@ -468,20 +542,30 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
     for (int i = 0; i < UPT; ++i)
       if (un.in[i]) {
         float* o = part + ((un.k_side[i] ? a.heads[0] : 0) + un.head[i]) * d;
+        float v[16];
+        elements_of<HALF>(v, dw[i]);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (owned<P, HALF>(j, lanes, e, d)) o[channel<P, HALF>(j, lanes, e, d)] = dw[i][e];
+          if (owned<P, HALF>(j, lanes, e, d)) o[channel<P, HALF>(j, lanes, e, d)] = v[e];
       }
     return;
   }
   float* by_warp = reinterpret_cast<float*>(ring);       // [warps][d]
   for (int t = 0; t < 2; ++t) {
     __syncthreads();
+    float sum[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < UPT; ++i) {
+      float v[16];
+      elements_of<HALF>(v, dw[i]);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum[e] += un.k_side[i] == (t == 1) ? v[e] : 0.f;
+    }
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      float v = 0.f;
-#pragma unroll
-      for (int i = 0; i < UPT; ++i) v += un.k_side[i] == (t == 1) ? dw[i][e] : 0.f;
+      float v = sum[e];
       // the heads of one warp, then the warps through shared memory
       for (int o = lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if ((int)(threadIdx.x & 31) < lanes && owned<P, HALF>(j, lanes, e, d))

@@ -45,13 +45,14 @@ struct Cursor {
 // is a whole group: its modulation gradients are final and written here, and
 // the weights' sums are added up over the block's units in `part`
 // [block][3][dim].
-template <typename XT, typename BT, int P, bool RING, int NV, int K, bool RES, bool NORM>
+// POST: the branch has a norm (0 no, 1 yes, 2 as the call says).
+template <typename XT, typename BT, int P, bool RING, int NV, int K, bool RES, bool NORM, int POST>
 __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
     row_bwd_kernel(const __grid_constant__ RowArgs a, int depth, bool weights) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Shared<K> sh;
   const int dim = a.dim, nwarps = blockDim.x >> 5;
-  const bool post = RES && a.post_norm != kNone, grad = a.dx_out != nullptr;
+  const bool post = RES && (POST == 2 ? a.post_norm != kNone : POST == 1), grad = a.dx_out != nullptr;
   const uint32_t xb = slot_bytes(blockDim.x, NV, sizeof(XT)), bb = slot_bytes(blockDim.x, NV, sizeof(BT));
   Stream<XT, P, RING, NV> sg{static_cast<const XT*>(a.dx_out), a.dx_out_stride, 0};
   Stream<BT, P, RING, NV> sy{static_cast<const BT*>(a.y), a.y_stride, xb};
@@ -98,25 +99,27 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
     Cursor c;
     c.enter(a, u);
     const long long g = a.chunks == 1 ? u : u / a.chunks;
-    float gate[NV][8], mul[NV][8];     // r gate pw, and (1 + s) w
-    float A[NV][8], B[NV][8], C[NV][8];
+    Eight gate[NV], times[NV];     // r gate pw, and (1 + s) w
+    Eight A[NV], B[NV], C[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float t[8];
+      Eight t;
       if (RES) {
         load_param<P>(gate[i], a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
         load_param<P>(t, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) gate[i][e] *= a.residual_scale * t[e];
+        for (int q = 0; q < 4; ++q)
+          gate[i].p[q] = present<P>(mul(gate[i].p[q], mul(both(a.residual_scale), t.p[q])), i, q, dim);
       }
       if (NORM) {
-        load_param<P>(mul[i], a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
+        load_param<P>(times[i], a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
         load_param<P>(t, a.weight, 0, a.param_bf16, 1.f, i, dim);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mul[i][e] = (1.f + mul[i][e]) * t[e];
+        for (int q = 0; q < 4; ++q) times[i].p[q] = mul(add(both(1.f), times[i].p[q]), t.p[q]);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) A[i][e] = B[i][e] = C[i][e] = 0.f;
+      A[i].fill(0.f);
+      B[i].fill(0.f);
+      C[i].fill(0.f);
     }
     for (long long r = c.r; r < c.end;) {
       const int n = c.end - r < K ? (int)(c.end - r) : K;
@@ -127,33 +130,28 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
         const int s = us + k >= depth ? us + k - depth : us + k;
         at[k] = ring + s * slot;
       }
-      float v[K][NV][8];               // x', then the gradient that reaches P
+      Eight v[K][NV];                  // x', then the gradient that reaches P (0 past the row's end)
       float ym[K], ys[K];
-      auto get_yhat = [&](float (&y)[8], int k, int i) {
+      auto get_yhat = [&](Eight& y, int k, int i) {
         sy.get(y, at[k], r + k, i, dim);
         if (post) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = column<P>(i, e) < dim ? (y[e] - ym[k]) * ys[k] : 0.f;
+          for (int q = 0; q < 4; ++q) y.p[q] = mul(add(y.p[q], both(-ym[k])), both(ys[k]));
         }
       };
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[k][i][e] = 0.f;
       if (post) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-          if (k < n) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) sy.get(v[k][i], at[k], r + k, i, dim);
+          for (int i = 0; i < NV; ++i) {
+            if (k < n) sy.get(v[k][i], at[k], r + k, i, dim);
+            else v[k][i].fill(0.f);
           }
         row_stats<P, NV, K>(v, a.post_norm, a.post_eps, dim, sh, half, nwarps, ym, ys);
       }
       float xm[K], xs[K], m0[K], m1[K];
       if (NORM) {
-        float w[K][NV][8];
+        Eight w[K][NV];
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -161,17 +159,17 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
             if (k < n) {
               sx.get(v[k][i], at[k], r + k, i, dim);
               if (RES) {
-                float y[8];
+                Eight y;
                 get_yhat(y, k, i);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[k][i][e] += gate[i][e] * y[e];
+                for (int q = 0; q < 4; ++q) v[k][i].p[q] = fma(gate[i].p[q], y.p[q], v[k][i].p[q]);
               }
               sd.get(w[k][i], at[k], r + k, i, dim);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) w[k][i][e] *= mul[i][e];
+              for (int q = 0; q < 4; ++q) w[k][i].p[q] = mul(w[k][i].p[q], times[i].p[q]);
             } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) w[k][i][e] = 0.f;
+              v[k][i].fill(0.f);
+              w[k][i].fill(0.f);
             }
           }
         row_stats_bwd<P, NV, K>(v, w, a.norm, a.eps, dim, sh, half, nwarps, xm, xs, m0, m1);
@@ -181,32 +179,29 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
         if (k >= n) break;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          float gr[8];
-          if (grad) {
-            sg.get(gr, at[k], r + k, i, dim);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) gr[e] = 0.f;
-          }
+          Eight gr;
+          if (grad) sg.get(gr, at[k], r + k, i, dim);
+          else gr.fill(0.f);
           if (NORM) {
-            float dh[8];
+            Eight dh;
             sd.get(dh, at[k], r + k, i, dim);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float xh = (v[k][i][e] - xm[k]) * xs[k];
-              A[i][e] += dh[e];
-              B[i][e] += dh[e] * xh;
-              gr[e] += xs[k] * (dh[e] * mul[i][e] - m0[k] - xh * m1[k]);
+            for (int q = 0; q < 4; ++q) {
+              const float2 xh = mul(add(v[k][i].p[q], both(-xm[k])), both(xs[k]));
+              A[i].p[q] = add(A[i].p[q], dh.p[q]);
+              B[i].p[q] = fma(dh.p[q], xh, B[i].p[q]);
+              const float2 u = fma(dh.p[q], times[i].p[q], both(-m0[k]));
+              gr.p[q] = fma(both(xs[k]), fma(xh, both(-m1[k]), u), gr.p[q]);
             }
             store8<P>(static_cast<XT*>(a.dx) + (r + k) * a.dx_stride, gr, i, dim);
           }
           if (RES) {
-            float y[8];
+            Eight y;
             get_yhat(y, k, i);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              C[i][e] += gr[e] * y[e];
-              v[k][i][e] = column<P>(i, e) < dim ? gr[e] * gate[i][e] : 0.f;
+            for (int q = 0; q < 4; ++q) {
+              C[i].p[q] = fma(gr.p[q], y.p[q], C[i].p[q]);
+              v[k][i].p[q] = mul(gr.p[q], gate[i].p[q]);
             }
             if (!post) store8<P>(static_cast<BT*>(a.dy) + (r + k) * a.dy_stride, v[k][i], i, dim);
           }
@@ -216,19 +211,21 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
         float t[2 * K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          t[k] = t[K + k] = 0.f;
+          float2 t0 = both(0.f), t1 = both(0.f);
           if (k < n) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-              float y[8];
+              Eight y;
               get_yhat(y, k, i);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                t[k] += v[k][i][e];
-                t[K + k] += v[k][i][e] * y[e];
+              for (int q = 0; q < 4; ++q) {
+                t0 = add(t0, v[k][i].p[q]);
+                t1 = fma(v[k][i].p[q], y.p[q], t1);
               }
             }
           }
+          t[k] = sum_of(t0);
+          t[K + k] = sum_of(t1);
         }
         block_sum(t, sh.sums, half, nwarps);
         const float inv_dim = 1.f / (float)dim;
@@ -238,10 +235,11 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
           const float p0 = a.post_norm == kLayer ? t[k] * inv_dim : 0.f, p1 = t[K + k] * inv_dim;
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
-            float y[8];
+            Eight y;
             get_yhat(y, k, i);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = ys[k] * (v[k][i][e] - p0 - y[e] * p1);
+            for (int q = 0; q < 4; ++q)
+              y.p[q] = mul(both(ys[k]), fma(y.p[q], both(-p1), add(v[k][i].p[q], both(-p0))));
             store8<P>(static_cast<BT*>(a.dy) + (r + k) * a.dy_stride, y, i, dim);
           }
         }
@@ -265,37 +263,33 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
       continue;
     }
     float* p = a.part + (long long)blockIdx.x * 3 * dim;
-    auto add_up = [&](float* to, const float (&t)[8], int i) {       // columns of this thread alone
-      float s[8];
-      if (first) {
+    auto add_up = [&](float* to, const Eight& t, int i) {       // columns of this thread alone
+      Eight s;
+      if (first) s.fill(0.f);
+      else load8<P>(s, to, i, dim);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] = 0.f;
-      } else {
-        load8<P>(s, to, i, dim);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += t[e];
+      for (int q = 0; q < 4; ++q) s.p[q] = add(s.p[q], t.p[q]);
       store8<P>(to, s, i, dim);
     };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float t[8], w[8], b[8];
+      Eight t, w, b;
       if (NORM) {
         load_param<P>(w, a.weight, 0, a.param_bf16, 1.f, i, dim);
         load_param<P>(b, a.bias, 0, a.param_bf16, 0.f, i, dim);
         if (a.dshift) store8<P>(a.dshift + g * dim, A[i], i, dim);
         if (a.dscale) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] = w[e] * B[i][e] + b[e] * A[i][e];
+          for (int q = 0; q < 4; ++q) t.p[q] = fma(w.p[q], B[i].p[q], mul(b.p[q], A[i].p[q]));
           store8<P>(a.dscale + g * dim, t, i, dim);
         }
         if (weights) {
           load_param<P>(b, a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] = (1.f + b[e]) * A[i][e];
+          for (int q = 0; q < 4; ++q) t.p[q] = mul(add(both(1.f), b.p[q]), A[i].p[q]);
           add_up(p, t, i);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] = (1.f + b[e]) * B[i][e];
+          for (int q = 0; q < 4; ++q) t.p[q] = mul(add(both(1.f), b.p[q]), B[i].p[q]);
           add_up(p + dim, t, i);
         }
       }
@@ -303,13 +297,13 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
         load_param<P>(w, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
         if (a.dgate) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] = a.residual_scale * w[e] * C[i][e];
+          for (int q = 0; q < 4; ++q) t.p[q] = mul(mul(both(a.residual_scale), w.p[q]), C[i].p[q]);
           store8<P>(a.dgate + g * dim, t, i, dim);
         }
         if (weights) {
           load_param<P>(b, a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] = a.residual_scale * b[e] * C[i][e];
+          for (int q = 0; q < 4; ++q) t.p[q] = mul(mul(both(a.residual_scale), b.p[q]), C[i].p[q]);
           add_up(p + 2 * (long long)dim, t, i);
         }
       }
@@ -320,7 +314,7 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 }
 
 // ----------------------------------------------------------------- launch --
-template <typename XT, typename BT, int P, bool RING, int NV, bool RES, bool NORM>
+template <typename XT, typename BT, int P, bool RING, int NV, bool RES, bool NORM, int POST>
 cudaError_t run(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
   constexpr int K = NV == 1 ? 2 : 1;
   const int threads = row_threads(a.dim, NV);
@@ -336,7 +330,7 @@ cudaError_t run(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
     if (depth < K) return cudaErrorInvalidConfiguration;
     smem = depth * slot;
   }
-  const auto kernel = row_bwd_kernel<XT, BT, P, RING, NV, K, RES, NORM>;
+  const auto kernel = row_bwd_kernel<XT, BT, P, RING, NV, K, RES, NORM, POST>;
   if (smem > 32 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -347,9 +341,11 @@ cudaError_t run(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
 
 template <typename XT, typename BT, int P, bool RING, int NV>
 cudaError_t by_op(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
-  if (a.dy && a.dh) return run<XT, BT, P, RING, NV, true, true>(a, grid, weights, s);
-  if (a.dy) return run<XT, BT, P, RING, NV, true, false>(a, grid, weights, s);
-  return run<XT, BT, P, RING, NV, false, true>(a, grid, weights, s);
+  if (a.dy && a.dh)
+    return a.post_norm == kNone ? run<XT, BT, P, RING, NV, true, true, 0>(a, grid, weights, s)
+                                : run<XT, BT, P, RING, NV, true, true, 1>(a, grid, weights, s);
+  if (a.dy) return run<XT, BT, P, RING, NV, true, false, 2>(a, grid, weights, s);
+  return run<XT, BT, P, RING, NV, false, true, 0>(a, grid, weights, s);
 }
 
 // Rows above 8192 elements are read where they are used.

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
   count_columns<P, NV>(sh.count, dim);
   int half = 0;
   long long group_end = r0;      // first row of the next modulation group
-  float gate[NV][8], mul[NV][8], add[NV][8];
+  Eight gate[NV], times[NV], plus[NV];
   for (long long r = r0; r < r1;) {
     if (r >= group_end) {
       const long long g = r / a.rows_per_group;
@@ -57,24 +57,24 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (RES) {
-          float pw[8];
+          Eight pw;
           load_param<P>(gate[i], a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
           load_param<P>(pw, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) gate[i][e] *= a.residual_scale * pw[e];
+          for (int q = 0; q < 4; ++q) gate[i].p[q] = mul(gate[i].p[q], mul(both(a.residual_scale), pw.p[q]));
         }
         if (NORM) {
           // (n w + b)(1 + s) + t = n (w (1 + s)) + (b (1 + s) + t)
-          float w[8], b[8];
-          load_param<P>(mul[i], a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
-          load_param<P>(add[i], a.shift, g * a.shift_stride, a.param_bf16, 0.f, i, dim);
+          Eight w, b;
+          load_param<P>(times[i], a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
+          load_param<P>(plus[i], a.shift, g * a.shift_stride, a.param_bf16, 0.f, i, dim);
           load_param<P>(w, a.weight, 0, a.param_bf16, 1.f, i, dim);
           load_param<P>(b, a.bias, 0, a.param_bf16, 0.f, i, dim);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float s1 = 1.f + mul[i][e];
-            add[i][e] += b[e] * s1;
-            mul[i][e] = w[e] * s1;
+          for (int q = 0; q < 4; ++q) {
+            const float2 s1 = add(both(1.f), times[i].p[q]);
+            plus[i].p[q] = fma(b.p[q], s1, plus[i].p[q]);
+            times[i].p[q] = mul(w.p[q], s1);
           }
         }
       }
@@ -88,38 +88,38 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
       const int s = us + k >= depth ? us + k - depth : us + k;
       at[k] = ring + s * slot;
     }
-    float x[K][NV][8];
+    Eight x[K][NV];
     if (RES) {
       float m[K], s[K];
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        m[k] = 0.f;
-        s[k] = 1.f;
+      for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          if (k < n) {
-            sy.get(x[k][i], at[k], r + k, i, dim);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[k][i][e] = 0.f;
-          }
+          if (k < n) sy.get(x[k][i], at[k], r + k, i, dim);
+          else x[k][i].fill(0.f);
         }
+      if (a.post_norm != kNone) {
+        row_stats<P, NV, K>(x, a.post_norm, a.post_eps, dim, sh, half, nwarps, m, s);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[k][i].p[q] = mul(add(x[k][i].p[q], both(-m[k])), both(s[k]));
       }
-      if (a.post_norm != kNone) row_stats<P, NV, K>(x, a.post_norm, a.post_eps, dim, sh, half, nwarps, m, s);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (k >= n) break;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          float v[8];
+          Eight v;
           sx.get(v, at[k], r + k, i, dim);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[k][i][e] = v[e] + gate[i][e] * ((x[k][i][e] - m[k]) * s[k]);
+          for (int q = 0; q < 4; ++q) x[k][i].p[q] = fma(gate[i].p[q], x[k][i].p[q], v.p[q]);
           store8<P>(static_cast<XT*>(a.x_out) + (r + k) * a.x_out_stride, x[k][i], i, dim);
           if (NORM) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (column<P>(i, e) >= dim) x[k][i][e] = 0.f;
+            for (int q = 0; q < 4; ++q) x[k][i].p[q] = present<P>(x[k][i].p[q], i, q, dim);
           }
         }
       }
@@ -128,12 +128,8 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          if (k < n) {
-            sx.get(x[k][i], at[k], r + k, i, dim);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[k][i][e] = 0.f;
-          }
+          if (k < n) sx.get(x[k][i], at[k], r + k, i, dim);
+          else x[k][i].fill(0.f);
         }
     }
     if (RING) {                 // everything of these rows is in registers: their slots are free
@@ -149,7 +145,8 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[k][i][e] = (x[k][i][e] - m[k]) * s[k] * mul[i][e] + add[i][e];
+          for (int q = 0; q < 4; ++q)
+            x[k][i].p[q] = fma(mul(add(x[k][i].p[q], both(-m[k])), both(s[k])), times[i].p[q], plus[i].p[q]);
           store8<P>(static_cast<BT*>(a.h) + (r + k) * a.h_stride, x[k][i], i, dim);
         }
       }

@@ -21,6 +21,13 @@ template <> struct Word<16> { using type = uint4; };
 struct alignas(16) Word32 { uint4 a, b; };
 template <> struct Word<32> { using type = Word32; };
 
+// Arithmetic on pairs: one instruction for two float32 operations.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float sum_of(float2 a) { return a.x + a.y; }
+
 // P neighbouring elements as one access.  bfloat16 is the upper half of a
 // float32: the low element of a word shifts up, the high one is masked.
 template <int P>

@@ -27,39 +27,52 @@ __device__ __forceinline__ int column(int i, int e) {
   return ((i * (8 / P) + e / P) * (int)blockDim.x + (int)threadIdx.x) * P + e % P;
 }
 
+// A thread's eight elements, as pairs.
+struct Eight {
+  float2 p[4];
+
+  __device__ __forceinline__ float* f() { return &p[0].x; }
+  __device__ __forceinline__ const float* f() const { return &p[0].x; }
+  __device__ __forceinline__ void fill(float v) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) p[q] = both(v);
+  }
+};
+
 template <int P, typename T>
-__device__ __forceinline__ void load8(float (&v)[8], const T* row, int i, int dim) {
+__device__ __forceinline__ void load8(Eight& v, const T* row, int i, int dim) {
 #pragma unroll
   for (int e = 0; e < 8; e += P) {
     const int c = column<P>(i, e);
     if (c < dim) {
-      load_piece<T, P>(v + e, row + c);
+      load_piece<T, P>(v.f() + e, row + c);
     } else {
 #pragma unroll
-      for (int q = 0; q < P; ++q) v[e + q] = 0.f;
+      for (int q = 0; q < P; ++q) v.f()[e + q] = 0.f;
     }
   }
 }
 template <int P, typename T>
-__device__ __forceinline__ void store8(T* row, const float (&v)[8], int i, int dim) {
+__device__ __forceinline__ void store8(T* row, const Eight& v, int i, int dim) {
 #pragma unroll
   for (int e = 0; e < 8; e += P) {
     const int c = column<P>(i, e);
-    if (c < dim) store_piece<P>(row + c, v + e);
+    if (c < dim) store_piece<P>(row + c, v.f() + e);
   }
 }
 // A parameter row in either type; absent ones read as `none`.
 template <int P>
-__device__ __forceinline__ void load_param(float (&v)[8], const void* p, long long off, bool is_bf16, float none, int i,
+__device__ __forceinline__ void load_param(Eight& v, const void* p, long long off, bool is_bf16, float none, int i,
                                            int dim) {
-  if (!p) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = none;
-  } else if (is_bf16) {
-    load8<P>(v, static_cast<const bf16*>(p) + off, i, dim);
-  } else {
-    load8<P>(v, static_cast<const float*>(p) + off, i, dim);
-  }
+  if (!p) v.fill(none);
+  else if (is_bf16) load8<P>(v, static_cast<const bf16*>(p) + off, i, dim);
+  else load8<P>(v, static_cast<const float*>(p) + off, i, dim);
+}
+// v in the columns of pair q that the row has, 0 in the others.
+template <int P>
+__device__ __forceinline__ float2 present(float2 v, int i, int q, int dim) {
+  if (P > 1) return column<P>(i, 2 * q) < dim ? v : both(0.f);
+  return make_float2(column<P>(i, 2 * q) < dim ? v.x : 0.f, column<P>(i, 2 * q + 1) < dim ? v.y : 0.f);
 }
 
 // One operand of the ring: its place in a slot, and where its rows come from.
@@ -91,11 +104,11 @@ struct Stream {
         if (c >= dim) reinterpret_cast<T*>(slot + at)[c] = T(0.f);
       }
   }
-  __device__ __forceinline__ void get(float (&v)[8], const unsigned char* slot, long long r, int i, int dim) const {
+  __device__ __forceinline__ void get(Eight& v, const unsigned char* slot, long long r, int i, int dim) const {
     if constexpr (RING) {
       const T* row = reinterpret_cast<const T*>(slot + at);
 #pragma unroll
-      for (int e = 0; e < 8; e += P) load_piece<T, P>(v + e, row + column<P>(i, e));
+      for (int e = 0; e < 8; e += P) load_piece<T, P>(v.f() + e, row + column<P>(i, e));
     } else {
       load8<P>(v, base + r * stride, i, dim);
     }
@@ -128,18 +141,19 @@ __device__ __forceinline__ void count_columns(float* count, int dim) {
 // mean and the warps' moments are merged (Chan, Golub and LeVeque, 1979), so
 // a row far from zero loses nothing and one barrier is enough.
 template <int P, int NV, int K>
-__device__ __forceinline__ void row_stats(const float (&v)[K][NV][8], int kind, float eps, int dim, Shared<K>& sh,
+__device__ __forceinline__ void row_stats(const Eight (&v)[K][NV], int kind, float eps, int dim, Shared<K>& sh,
                                           int& half, int nwarps, float (&mean)[K], float (&rstd)[K]) {
   const float inv_dim = 1.f / (float)dim;
   float s[K];
   if (kind == kRms) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      s[k] = 0.f;
+      float2 t = both(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[k] += v[k][i][e] * v[k][i][e];
+        for (int q = 0; q < 4; ++q) t = fma(v[k][i].p[q], v[k][i].p[q], t);
+      s[k] = sum_of(t);
     }
     block_sum(s, sh.sums, half, nwarps);
 #pragma unroll
@@ -154,25 +168,27 @@ __device__ __forceinline__ void row_stats(const float (&v)[K][NV][8], int kind, 
   const float n = sh.count[warp];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    s[k] = 0.f;
+    float2 t = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[k] += v[k][i][e];
+      for (int q = 0; q < 4; ++q) t = add(t, v[k][i].p[q]);
+    s[k] = sum_of(t);
   }
   const float own = n > 0.f ? warp_sum_spread<K>(s) / n : 0.f;      // of the row this lane stands for
   float m[K];
   spread_get<K>(m, own);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    s[k] = 0.f;
+    float2 t = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float t = column<P>(i, e) < dim ? v[k][i][e] - m[k] : 0.f;
-        s[k] += t * t;
+      for (int q = 0; q < 4; ++q) {
+        const float2 off = add(v[k][i].p[q], present<P>(both(-m[k]), i, q, dim));
+        t = fma(off, off, t);
       }
+    s[k] = sum_of(t);
   }
   float q = warp_sum_spread<K>(s);
   float mu = own;
@@ -206,7 +222,7 @@ __device__ __forceinline__ void row_stats(const float (&v)[K][NV][8], int kind, 
 // mean(u) (0 for the rms norm) and mean(u xhat), with one barrier: the sums
 // with u are taken about the warps' means as well and merged alike.
 template <int P, int NV, int K>
-__device__ __forceinline__ void row_stats_bwd(const float (&v)[K][NV][8], const float (&u)[K][NV][8], int kind, float eps,
+__device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][NV], const Eight (&u)[K][NV], int kind, float eps,
                                               int dim, Shared<K>& sh, int& half, int nwarps, float (&mean)[K],
                                               float (&rstd)[K], float (&mu0)[K], float (&mu1)[K]) {
   const float inv_dim = 1.f / (float)dim;
@@ -214,14 +230,16 @@ __device__ __forceinline__ void row_stats_bwd(const float (&v)[K][NV][8], const 
   if (kind == kRms) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      s[k] = s[K + k] = 0.f;
+      float2 t0 = both(0.f), t1 = both(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s[k] += v[k][i][e] * v[k][i][e];
-          s[K + k] += u[k][i][e] * v[k][i][e];
+        for (int q = 0; q < 4; ++q) {
+          t0 = fma(v[k][i].p[q], v[k][i].p[q], t0);
+          t1 = fma(u[k][i].p[q], v[k][i].p[q], t1);
         }
+      s[k] = sum_of(t0);
+      s[K + k] = sum_of(t1);
     }
     block_sum(s, sh.sums, half, nwarps);
 #pragma unroll
@@ -239,14 +257,16 @@ __device__ __forceinline__ void row_stats_bwd(const float (&v)[K][NV][8], const 
   const float n = sh.count[warp], inv_n = n > 0.f ? 1.f / n : 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    s[k] = s[K + k] = 0.f;
+    float2 t0 = both(0.f), t1 = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s[k] += v[k][i][e];
-        s[K + k] += u[k][i][e];
+      for (int q = 0; q < 4; ++q) {
+        t0 = add(t0, v[k][i].p[q]);
+        t1 = add(t1, u[k][i].p[q]);
       }
+    s[k] = sum_of(t0);
+    s[K + k] = sum_of(t1);
   }
   float first = warp_sum_spread<N>(s);
   if (lane < 16) first *= inv_n;                 // lanes below 16 stand for x', the others for u
@@ -254,15 +274,17 @@ __device__ __forceinline__ void row_stats_bwd(const float (&v)[K][NV][8], const 
   spread_get<N>(m, first);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    s[k] = s[K + k] = 0.f;
+    float2 t0 = both(0.f), t1 = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float t = column<P>(i, e) < dim ? v[k][i][e] - m[k] : 0.f;
-        s[k] += t * t;
-        s[K + k] += u[k][i][e] * t;
+      for (int q = 0; q < 4; ++q) {
+        const float2 off = add(v[k][i].p[q], present<P>(both(-m[k]), i, q, dim));
+        t0 = fma(off, off, t0);
+        t1 = fma(u[k][i].p[q], off, t1);
       }
+    s[k] = sum_of(t0);
+    s[K + k] = sum_of(t1);
   }
   float second = warp_sum_spread<N>(s);
   float mu = first;

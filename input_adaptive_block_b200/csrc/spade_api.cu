@@ -408,6 +408,15 @@ spade_status check_scratch(const void* workspace, size_t ws_bytes, size_t need) 
   return SPADE_OK;
 }
 
+// by = 1 .. 2^31 - 1: with 2^s the power of two at or above it, the multiplier
+// 2^(31 + s) / by rounded up past the quotient is below 2^32 and off by at
+// most one, which 2^31 multiples of it do not carry over 2^(31 + s) / by.
+QkArgs::Divisor divisor(unsigned by) {
+  unsigned s = 0;
+  while ((1ULL << s) < by) ++s;
+  return {by, (unsigned)((1ULL << (31 + s)) / by + 1), 31 + s};
+}
+
 // Sizes, types, strides and rotation of a Q/K pass; rope == nullptr skips the
 // rotation and the grid (workspace query).
 spade_status plan_qk(const spade_qk_desc* D, const spade_rope* rope, const int32_t* positions, QkArgs& a) {
@@ -459,7 +468,7 @@ spade_status plan_qk(const spade_qk_desc* D, const spade_rope* rope, const int32
     a.axis[i] = (uint8_t)rope->axis[i];
     a.turn[i] = rope->freq[i] / 6.283185307179586476925286766559;
   }
-  a.H = a.W = 1;
+  a.H = a.W = divisor(1);
   if (positions) {
     if (d.text_tokens) return fail(SPADE_ERR_INVALID, "text_tokens with positions");
     if (reinterpret_cast<uintptr_t>(positions) % 4) return fail(SPADE_ERR_INVALID, "positions are not aligned to their type");
@@ -472,8 +481,8 @@ spade_status plan_qk(const spade_qk_desc* D, const spade_rope* rope, const int32
       return fail(SPADE_ERR_INVALID, "rows past the end of the grid: offset %lld, %lld rows, %lld tokens",
                   (long long)d.token_offset, a.video_rows, plane * d.T);
     a.tok0 = (int)d.token_offset;
-    a.H = d.H;
-    a.W = d.W;
+    a.H = divisor((unsigned)d.H);
+    a.W = divisor((unsigned)d.W);
   }
   return SPADE_OK;
 }

@@ -135,7 +135,11 @@ cudaError_t launch_row_bwd(const RowArgs& a, int grid, cudaStream_t s);
 // tensor without heads is absent.
 struct QkArgs {
   long long rows, video_rows;
-  int tok0, H, W;                  // grid position of row 0 (no positions given)
+  struct Divisor {                 // n / by = n * mul >> shift for n below 2^31
+    unsigned by, mul, shift;
+  };
+  int tok0;                        // grid token of row 0 (no positions given)
+  Divisor H, W;
   int heads[2], d, lanes;          // lanes: threads per head, a power of two
   int norm;
   float eps;
