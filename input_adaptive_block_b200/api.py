@@ -372,21 +372,21 @@ class RowGrads(NamedTuple):
 class _On:
     """Makes `like`'s device and, when given, `stream` current for a call, so
     that what it allocates belongs to the stream it runs on."""
+    __slots__ = ("ctx", "device")
 
     def __init__(self, like: torch.Tensor, stream):
-        if stream is not None and stream.device != like.device:
-            raise ValueError(f"stream of {stream.device} for tensors of {like.device}")
+        self.ctx, self.device = None, like.get_device()
         if stream is not None:
+            if stream.device != like.device:
+                raise ValueError(f"stream of {stream.device} for tensors of {like.device}")
             self.ctx = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != like.device.index:
-            self.ctx = torch.cuda.device(like.device)
-        else:
-            self.ctx = None
+        elif torch.cuda.current_device() != self.device:
+            self.ctx = torch.cuda.device(self.device)
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device)
 
     def __exit__(self, *exc):
         return self.ctx.__exit__(*exc) if self.ctx is not None else None
@@ -399,11 +399,20 @@ def _on_gpu(t: torch.Tensor, name: str, like: torch.Tensor) -> None:
         raise ValueError(f"{name} is on {t.device}, not on {like.device}")
 
 
+def _new(like: torch.Tensor, shape, dtype) -> torch.Tensor:
+    """A packed tensor on like's device."""
+    if like.dtype is dtype and like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _strided(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dtype) -> Tuple[Optional[int], int]:
     """(pointer, row stride) of a tensor of rows [rows, ...] whose rows are
     packed inside and may lie any distance apart."""
     if t is None:
         return None, 0
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda and t.get_device() == like.get_device():
+        return t.data_ptr(), 0
     _on_gpu(t, name, like)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
@@ -433,10 +442,13 @@ def _vector(t: Optional[torch.Tensor], name: str, like: torch.Tensor, n: int, dt
 
 
 def _param_dtype(params) -> torch.dtype:
-    given = [t.dtype for t in params if t is not None]
-    if any(dt != given[0] for dt in given):
-        raise TypeError(f"parameters of several dtypes: {given}")
-    return given[0] if given else torch.float32
+    dt = None
+    for t in params:
+        if t is not None and t.dtype is not dt:
+            if dt is not None:
+                raise TypeError(f"parameters of several dtypes: {dt}, {t.dtype}")
+            dt = t.dtype
+    return dt or torch.float32
 
 
 def _scratch(workspace, need: int, like: torch.Tensor) -> Tuple[Optional[int], int, Optional[torch.Tensor]]:
@@ -509,9 +521,9 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: Spa
     desc, like, pos, (qw, kw) = _qk_desc(q, k, q_weight, k_weight, grid, positions, token_offset, text_tokens, norm, eps)
     with _On(like, stream) as s:
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _new(q, q.shape, q.dtype)
         if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            k_out = _new(k, k.shape, k.dtype)
         rows, d, dt = desc.rows, desc.d, like.dtype
         qs, ks = (rows, desc.q_heads, d), (rows, desc.k_heads, d)
         qp, desc.q_stride = _strided(q, "q", like, qs, dt)
@@ -546,9 +558,9 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
         rows, d, dt = desc.rows, desc.d, like.dtype
         qs, ks = (rows, desc.q_heads, d), (rows, desc.k_heads, d)
         if dq_out is not None and dq is None:
-            dq = torch.empty(qs, dtype=dt, device=like.device)
+            dq = _new(dq_out, qs, dt)
         if dk_out is not None and dk is None:
-            dk = torch.empty(ks, dtype=dt, device=like.device)
+            dk = _new(dk_out, ks, dt)
         gq, desc.q_dout_stride = _strided(dq_out, "dq_out", like, qs, dt)
         gk, desc.k_dout_stride = _strided(dk_out, "dk_out", like, ks, dt)
         normed = norm != "none"
@@ -556,8 +568,7 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
         kp, desc.k_stride = _strided(k if normed and dk_out is not None else None, "k", like, ks, dt)
         qo, desc.q_out_stride = _strided(dq if dq_out is not None else None, "dq", like, qs, dt)
         ko, desc.k_out_stride = _strided(dk if dk_out is not None else None, "dk", like, ks, dt)
-        dqw, dkw = (None if w is None else torch.empty(w.shape, dtype=torch.float32, device=like.device)
-                    for w in (q_weight, k_weight))
+        dqw, dkw = (None if w is None else _new(w, w.shape, torch.float32) for w in (q_weight, k_weight))
         lib = _lib.load()
         need = int(lib.spade_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(desc))) if dqw is not None or dkw is not None else 0
         wp, wn, workspace = _scratch(workspace, need, like)
@@ -579,24 +590,25 @@ def _row_call(like, x_dtype, branch_dtype, norm="none", eps=0.0, post_norm="none
     given = {"gate": gate, "post_weight": post_weight, "weight": weight, "bias": bias, "scale": scale, "shift": shift}
     pdt = _param_dtype(given.values())
     groups = None
-    for name in ("gate", "scale", "shift"):
-        t = given[name]
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
         if t is None:
             continue
         if t.dim() not in (1, 2) or t.shape[-1] != dim:
             raise ValueError(f"{name} must be [groups, {dim}] or [{dim}]")
         g = t.shape[0] if t.dim() == 2 else 1
-        if groups not in (None, g):
+        if groups is not None and groups != g:
             raise ValueError("gate, scale and shift must have one number of groups")
         groups = g
         p, stride = _strided(t if t.dim() == 2 else t.unsqueeze(0), name, like, (g, dim), pdt)
         setattr(params, name, p)
-        setattr(desc, name + "_stride", stride)
+        if stride:
+            setattr(desc, name + "_stride", stride)
     groups = 1 if groups is None else groups
     if groups < 1 or rows % groups:
         raise ValueError(f"{rows} rows in {groups} groups")
-    for name in ("post_weight", "weight", "bias"):
-        setattr(params, name, _vector(given[name], name, like, dim, pdt))
+    for name, t in (("post_weight", post_weight), ("weight", weight), ("bias", bias)):
+        if t is not None:
+            setattr(params, name, _vector(t, name, like, dim, pdt))
     desc.rows, desc.groups, desc.dim = rows, groups, dim
     desc.x_dt, desc.branch_dt, desc.param_dt = dtype_code(x_dtype), dtype_code(branch_dtype), dtype_code(pdt)
     desc.norm, desc.post_norm = _code(NORM, norm, "norm"), _code(NORM, post_norm, "post_norm")
@@ -606,9 +618,13 @@ def _row_call(like, x_dtype, branch_dtype, norm="none", eps=0.0, post_norm="none
 
 def _row_grads(given, like):
     """Float32 gradient tensors of the parameters given, and their table."""
-    out = {n: None if given[n] is None else torch.empty(given[n].shape, dtype=torch.float32, device=like.device)
-           for n in ROW_PARAMS}
-    return out, SpadeRowGrads(**{n: None if t is None else t.data_ptr() for n, t in out.items()})
+    out, table = {}, SpadeRowGrads()
+    for n in ROW_PARAMS:
+        t = given[n]
+        out[n] = t if t is None else _new(t, t.shape, torch.float32)
+        if t is not None:
+            setattr(table, n, out[n].data_ptr())
+    return out, table
 
 
 def row_workspace_bytes(rows: int, dim: int, groups: int = 1) -> int:
@@ -631,7 +647,7 @@ def norm_modulate(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
     desc, params, _ = _row_call(x, x.dtype, odt, norm, eps, weight=weight, bias=bias, scale=scale, shift=shift)
     with _On(x, stream) as s:
         if out is None:
-            out = torch.empty(x.shape, dtype=odt, device=x.device)
+            out = _new(x, x.shape, odt)
         xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
         op, desc.h_stride = _strided(out, "out", x, x.shape, odt)
         check(_lib.load().spade_norm_modulate(ctypes.byref(desc), ctypes.byref(params), xp, op, s), "spade_norm_modulate")
@@ -649,7 +665,7 @@ def norm_modulate_backward(dout: torch.Tensor, x: torch.Tensor, weight: Optional
     desc, params, given = _row_call(x, x.dtype, dout.dtype, norm, eps, weight=weight, bias=bias, scale=scale, shift=shift)
     with _On(x, stream) as s:
         if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            dx = _new(x, x.shape, x.dtype)
         xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
         hp, desc.dh_stride = _strided(dout, "dout", x, x.shape, dout.dtype)
         rp, desc.dx_out_stride = _strided(dres, "dres", x, x.shape, x.dtype)
@@ -672,7 +688,7 @@ def gate_residual(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor]
                                 residual_scale=residual_scale, gate=gate, post_weight=post_weight)
     with _On(x, stream) as s:
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = _new(x, x.shape, x.dtype)
         xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
         yp, desc.y_stride = _strided(y, "y", x, x.shape, y.dtype)
         op, desc.x_out_stride = _strided(out, "out", x, x.shape, x.dtype)
@@ -691,7 +707,7 @@ def gate_residual_backward(dout: torch.Tensor, y: torch.Tensor, gate: Optional[t
                                     residual_scale=residual_scale, gate=gate, post_weight=post_weight)
     with _On(dout, stream) as s:
         if dy is None:
-            dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+            dy = _new(y, y.shape, y.dtype)
         gp, desc.dx_out_stride = _strided(dout, "dout", dout, dout.shape, dout.dtype)
         yp, desc.y_stride = _strided(y, "y", dout, dout.shape, y.dtype)
         dp, desc.dy_stride = _strided(dy, "dy", dout, dout.shape, y.dtype)
@@ -717,9 +733,9 @@ def gate_residual_norm(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Te
                                 weight, bias, scale, shift)
     with _On(x, stream) as s:
         if x_out is None:
-            x_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            x_out = _new(x, x.shape, x.dtype)
         if out is None:
-            out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+            out = _new(y, y.shape, y.dtype)
         xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
         yp, desc.y_stride = _strided(y, "y", x, x.shape, y.dtype)
         op, desc.x_out_stride = _strided(x_out, "x_out", x, x.shape, x.dtype)
@@ -744,9 +760,9 @@ def gate_residual_norm_backward(dx_out: Optional[torch.Tensor], dout: torch.Tens
                                     weight, bias, scale, shift)
     with _On(x, stream) as s:
         if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            dx = _new(x, x.shape, x.dtype)
         if dy is None:
-            dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+            dy = _new(y, y.shape, y.dtype)
         gp, desc.dx_out_stride = _strided(dx_out, "dx_out", x, x.shape, x.dtype)
         hp, desc.dh_stride = _strided(dout, "dout", x, x.shape, y.dtype)
         xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)

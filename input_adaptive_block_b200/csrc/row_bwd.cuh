@@ -24,18 +24,21 @@ using namespace rowpass;
 
 // A unit is chunk c of group g: rows [g R + R c / C, g R + R (c + 1) / C) of a
 // group of R rows cut into C chunks.
-struct Cursor {
-  long long unit, r, end;
+struct Run {
+  long long group, first;
+  int rows;
 
-  __device__ __forceinline__ void enter(const RowArgs& a, long long u) {
-    unit = u;
+  __device__ __forceinline__ Run(const RowArgs& a, long long u) {
     if (a.chunks == 1) {
-      r = u * a.rows_per_group;
-      end = r + a.rows_per_group;
+      group = u;
+      first = u * a.rows_per_group;
+      rows = (int)a.rows_per_group;
     } else {
-      const long long g = u / a.chunks, c = u - g * a.chunks, base = g * a.rows_per_group;
-      r = base + a.rows_per_group * c / a.chunks;
-      end = base + a.rows_per_group * (c + 1) / a.chunks;
+      const long long c = u % a.chunks;
+      group = u / a.chunks;
+      const long long from = a.rows_per_group * c / a.chunks, to = a.rows_per_group * (c + 1) / a.chunks;
+      first = group * a.rows_per_group + from;
+      rows = (int)(to - from);
     }
   }
 };
@@ -50,35 +53,65 @@ template <typename XT, typename BT, int P, bool RING, int NV, int K, bool RES, b
 __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
     row_bwd_kernel(const __grid_constant__ RowArgs a, int depth, bool weights) {
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ Shared<K> sh;
+  __shared__ Shared<2 * K> sh;
   const int dim = a.dim, nwarps = blockDim.x >> 5;
   const bool post = RES && (POST == 2 ? a.post_norm != kNone : POST == 1), grad = a.dx_out != nullptr;
   const uint32_t xb = slot_bytes(blockDim.x, NV, sizeof(XT)), bb = slot_bytes(blockDim.x, NV, sizeof(BT));
-  Stream<XT, P, RING, NV> sg{static_cast<const XT*>(a.dx_out), a.dx_out_stride, 0};
-  Stream<BT, P, RING, NV> sy{static_cast<const BT*>(a.y), a.y_stride, xb};
-  Stream<XT, P, RING, NV> sx{static_cast<const XT*>(a.x), a.x_stride, xb + (RES ? bb : 0)};
-  Stream<BT, P, RING, NV> sd{static_cast<const BT*>(a.dh), a.dh_stride, sx.at + xb};
-  const uint32_t slot = NORM ? sd.at + bb : sx.at;
+  Stream<XT, P, RING, NV> sg, sx;
+  Stream<BT, P, RING, NV> sy, sd;
+  sg.at = 0;
+  sy.at = xb;
+  sx.at = xb + (RES ? bb : 0);
+  sd.at = sx.at + xb;
+  const uint32_t slot = NORM ? sd.at + bb : sx.at, ring_bytes = depth * slot;
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
   const long long units = a.groups * a.chunks;
+  auto seek = [&](long long r) {
+    sg.seek(a.dx_out, a.dx_out_stride, r);
+    if (RES) sy.seek(a.y, a.y_stride, r);
+    if (NORM) {
+      sx.seek(a.x, a.x_stride, r);
+      sd.seek(a.dh, a.dh_stride, r);
+    }
+  };
+  auto advance = [&](int n) {
+    sg.p += n * a.dx_out_stride;
+    if (RES) sy.p += n * a.y_stride;
+    if (NORM) {
+      sx.p += n * a.x_stride;
+      sd.p += n * a.dh_stride;
+    }
+  };
 
-  Cursor f;                      // the next row to copy
-  int fs = 0, us = 0;            // its slot; the slot of the next row to use
-  f.enter(a, blockIdx.x);
+  long long fu = blockIdx.x;     // the unit of the next row to copy, and its rows to copy
+  int to_copy = 0;
+  uint32_t fs = 0, us = 0;       // slot of the next row to copy, of the next to use
+  if (RING && fu < units) {
+    const Run f(a, fu);
+    seek(f.first);
+    to_copy = f.rows;
+  }
   auto fetch = [&]() {
-    if (f.unit < units) {
-      const uint32_t to = ring_at + fs * slot;
-      if (grad) sg.fetch(to, f.r, dim);
-      if (RES) sy.fetch(to, f.r, dim);
+    if (to_copy > 0) {
+      const uint32_t to = ring_at + fs;
+      if (grad) sg.fetch(to, dim);
+      if (RES) sy.fetch(to, dim);
       if (NORM) {
-        sx.fetch(to, f.r, dim);
-        sd.fetch(to, f.r, dim);
+        sx.fetch(to, dim);
+        sd.fetch(to, dim);
       }
-      if (++f.r == f.end && f.unit + gridDim.x < units) f.enter(a, f.unit + gridDim.x);
-      else if (f.r == f.end) f.unit = units;
+      advance(1);
+      if (--to_copy == 0) {
+        fu += gridDim.x;
+        if (fu < units) {
+          const Run f(a, fu);
+          seek(f.first);
+          to_copy = f.rows;
+        }
+      }
     }
     commit_async();
-    fs = fs + 1 == depth ? 0 : fs + 1;
+    fs = fs + slot == ring_bytes ? 0 : fs + slot;
   };
   if (RING) {
     for (int d = 0; d < depth; ++d) {
@@ -96,9 +129,11 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
   int half = 0;
   bool first = true;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    Cursor c;
-    c.enter(a, u);
-    const long long g = a.chunks == 1 ? u : u / a.chunks;
+    const Run run(a, u);
+    const long long g = run.group;
+    if (!RING) seek(run.first);
+    XT* dxo = NORM ? static_cast<XT*>(a.dx) + run.first * a.dx_stride : nullptr;
+    BT* dyo = RES ? static_cast<BT*>(a.dy) + run.first * a.dy_stride : nullptr;
     Eight gate[NV], times[NV];     // r gate pw, and (1 + s) w
     Eight A[NV], B[NV], C[NV];
 #pragma unroll
@@ -121,19 +156,16 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
       B[i].fill(0.f);
       C[i].fill(0.f);
     }
-    for (long long r = c.r; r < c.end;) {
-      const int n = c.end - r < K ? (int)(c.end - r) : K;
+    for (int left = run.rows; left > 0;) {
+      const int n = left < K ? left : K;
       if (RING) wait_async_upto(depth - K);
       const unsigned char* at[K];
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int s = us + k >= depth ? us + k - depth : us + k;
-        at[k] = ring + s * slot;
-      }
+      for (int k = 0; k < K; ++k) at[k] = ring + (us + k * slot >= ring_bytes ? us + k * slot - ring_bytes : us + k * slot);
       Eight v[K][NV];                  // x', then the gradient that reaches P (0 past the row's end)
       float ym[K], ys[K];
       auto get_yhat = [&](Eight& y, int k, int i) {
-        sy.get(y, at[k], r + k, i, dim);
+        sy.get(y, at[k], k * a.y_stride, i, dim);
         if (post) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) y.p[q] = mul(add(y.p[q], both(-ym[k])), both(ys[k]));
@@ -144,7 +176,7 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
         for (int k = 0; k < K; ++k)
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
-            if (k < n) sy.get(v[k][i], at[k], r + k, i, dim);
+            if (k < n) sy.get(v[k][i], at[k], k * a.y_stride, i, dim);
             else v[k][i].fill(0.f);
           }
         row_stats<P, NV, K>(v, a.post_norm, a.post_eps, dim, sh, half, nwarps, ym, ys);
@@ -157,14 +189,14 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
             if (k < n) {
-              sx.get(v[k][i], at[k], r + k, i, dim);
+              sx.get(v[k][i], at[k], k * a.x_stride, i, dim);
               if (RES) {
                 Eight y;
                 get_yhat(y, k, i);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[k][i].p[q] = fma(gate[i].p[q], y.p[q], v[k][i].p[q]);
               }
-              sd.get(w[k][i], at[k], r + k, i, dim);
+              sd.get(w[k][i], at[k], k * a.dh_stride, i, dim);
 #pragma unroll
               for (int q = 0; q < 4; ++q) w[k][i].p[q] = mul(w[k][i].p[q], times[i].p[q]);
             } else {
@@ -180,11 +212,11 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           Eight gr;
-          if (grad) sg.get(gr, at[k], r + k, i, dim);
+          if (grad) sg.get(gr, at[k], k * a.dx_out_stride, i, dim);
           else gr.fill(0.f);
           if (NORM) {
             Eight dh;
-            sd.get(dh, at[k], r + k, i, dim);
+            sd.get(dh, at[k], k * a.dh_stride, i, dim);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float2 xh = mul(add(v[k][i].p[q], both(-xm[k])), both(xs[k]));
@@ -193,7 +225,7 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
               const float2 u = fma(dh.p[q], times[i].p[q], both(-m0[k]));
               gr.p[q] = fma(both(xs[k]), fma(xh, both(-m1[k]), u), gr.p[q]);
             }
-            store8<P>(static_cast<XT*>(a.dx) + (r + k) * a.dx_stride, gr, i, dim);
+            store8<P>(dxo + k * a.dx_stride, gr, i, dim);
           }
           if (RES) {
             Eight y;
@@ -203,7 +235,7 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
               C[i].p[q] = fma(gr.p[q], y.p[q], C[i].p[q]);
               v[k][i].p[q] = mul(gr.p[q], gate[i].p[q]);
             }
-            if (!post) store8<P>(static_cast<BT*>(a.dy) + (r + k) * a.dy_stride, v[k][i], i, dim);
+            if (!post) store8<P>(dyo + k * a.dy_stride, v[k][i], i, dim);
           }
         }
       }
@@ -240,15 +272,19 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               y.p[q] = mul(both(ys[k]), fma(y.p[q], both(-p1), add(v[k][i].p[q], both(-p0))));
-            store8<P>(static_cast<BT*>(a.dy) + (r + k) * a.dy_stride, y, i, dim);
+            store8<P>(dyo + k * a.dy_stride, y, i, dim);
           }
         }
       }
       if (RING) {
         for (int k = 0; k < n; ++k) fetch();
-        us = us + n >= depth ? us + n - depth : us + n;
+        us = us + n * slot >= ring_bytes ? us + n * slot - ring_bytes : us + n * slot;
+      } else {
+        advance(n);
       }
-      r += n;
+      if (NORM) dxo += n * a.dx_stride;
+      if (RES) dyo += n * a.dy_stride;
+      left -= n;
     }
     if (a.chunks > 1) {
       float* p = a.part + u * 3 * dim;
@@ -316,14 +352,14 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 // ----------------------------------------------------------------- launch --
 template <typename XT, typename BT, int P, bool RING, int NV, bool RES, bool NORM, int POST>
 cudaError_t run(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
-  constexpr int K = NV == 1 ? 2 : 1;
+  constexpr int K = NV == 1 && POST != 1 ? 2 : 1;
   const int threads = row_threads(a.dim, NV);
   const size_t slot = slot_bytes(threads, NV, sizeof(XT)) * (NORM ? 2 : 1) +
                       slot_bytes(threads, NV, sizeof(BT)) * ((RES ? 1 : 0) + (NORM ? 1 : 0));
   int depth = 0;
   size_t smem = 0;
   if (RING) {
-    const size_t room = kSmemSm / bwd_blocks(a.dim) - 1024 - sizeof(Shared<K>);
+    const size_t room = kSmemSm / bwd_blocks(a.dim) - 1024 - sizeof(Shared<2 * K>);
     const long long rows = (a.rows + grid - 1) / grid;
     depth = (int)(room / slot < kDepthMax ? room / slot : kDepthMax);
     if (rows < depth) depth = (int)(rows > K ? rows : K);

@@ -16,28 +16,38 @@ namespace {
 
 using namespace rowpass;
 
-template <typename XT, typename BT, int P, bool RING, int NV, int K, bool RES, bool NORM>
+// POST: the branch has a norm (0 no, 1 yes, 2 as the call says).
+template <typename XT, typename BT, int P, bool RING, int NV, int K, bool RES, bool NORM, int POST>
 __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const __grid_constant__ RowArgs a, int depth) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Shared<K> sh;
   const int dim = a.dim, nwarps = blockDim.x >> 5;
-  Stream<XT, P, RING, NV> sx{static_cast<const XT*>(a.x), a.x_stride, 0};
-  Stream<BT, P, RING, NV> sy{static_cast<const BT*>(a.y), a.y_stride, slot_bytes(blockDim.x, NV, sizeof(XT))};
-  const uint32_t slot = sy.at + (RES ? slot_bytes(blockDim.x, NV, sizeof(BT)) : 0);
-  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
   const long long r0 = a.rows * blockIdx.x / gridDim.x, r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
+  Stream<XT, P, RING, NV> sx;
+  Stream<BT, P, RING, NV> sy;
+  sx.seek(a.x, a.x_stride, r0);
+  sx.at = 0;
+  sy.at = slot_bytes(blockDim.x, NV, sizeof(XT));
+  if (RES) sy.seek(a.y, a.y_stride, r0);
+  XT* xo = RES ? static_cast<XT*>(a.x_out) + r0 * a.x_out_stride : nullptr;
+  BT* ho = NORM ? static_cast<BT*>(a.h) + r0 * a.h_stride : nullptr;
+  const uint32_t slot = sy.at + (RES ? slot_bytes(blockDim.x, NV, sizeof(BT)) : 0), ring_bytes = depth * slot;
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
 
-  // the next row to copy and its slot; the slot of the next row to use
-  long long fr = r0;
-  int fs = 0, us = 0;
+  int left = (int)(r1 - r0), to_copy = left;   // rows to use, and to copy
+  uint32_t fs = 0, us = 0;                     // slot of the next row to copy, of the next to use
   auto fetch = [&]() {
-    if (fr < r1) {
-      sx.fetch(ring_at + fs * slot, fr, dim);
-      if (RES) sy.fetch(ring_at + fs * slot, fr, dim);
+    if (to_copy > 0) {
+      sx.fetch(ring_at + fs, dim);
+      sx.p += a.x_stride;
+      if (RES) {
+        sy.fetch(ring_at + fs, dim);
+        sy.p += a.y_stride;
+      }
     }
     commit_async();
-    ++fr;
-    fs = fs + 1 == depth ? 0 : fs + 1;
+    --to_copy;
+    fs = fs + slot == ring_bytes ? 0 : fs + slot;
   };
   if (RING) {
     for (int d = 0; d < depth; ++d) {
@@ -48,12 +58,14 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
   }
   count_columns<P, NV>(sh.count, dim);
   int half = 0;
-  long long group_end = r0;      // first row of the next modulation group
+  long long g = r0 / a.rows_per_group - 1;
+  int of_group = 0;              // rows until the next modulation group
   Eight gate[NV], times[NV], plus[NV];
-  for (long long r = r0; r < r1;) {
-    if (r >= group_end) {
-      const long long g = r / a.rows_per_group;
-      group_end = (g + 1) * a.rows_per_group;
+  while (left > 0) {
+    if (of_group == 0) {
+      ++g;
+      const long long end = (g + 1) * a.rows_per_group;
+      of_group = (int)((end < r1 ? end : r1) - (r1 - left));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (RES) {
@@ -61,7 +73,8 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
           load_param<P>(gate[i], a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
           load_param<P>(pw, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) gate[i].p[q] = mul(gate[i].p[q], mul(both(a.residual_scale), pw.p[q]));
+          for (int q = 0; q < 4; ++q)
+            gate[i].p[q] = present<P>(mul(gate[i].p[q], mul(both(a.residual_scale), pw.p[q])), i, q, dim);
         }
         if (NORM) {
           // (n w + b)(1 + s) + t = n (w (1 + s)) + (b (1 + s) + t)
@@ -79,26 +92,22 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
         }
       }
     }
-    const long long end = r1 < group_end ? r1 : group_end;
-    const int n = end - r < K ? (int)(end - r) : K;
+    const int n = of_group < K ? of_group : K;
     if (RING) wait_async_upto(depth - K);
     const unsigned char* at[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int s = us + k >= depth ? us + k - depth : us + k;
-      at[k] = ring + s * slot;
-    }
-    Eight x[K][NV];
+    for (int k = 0; k < K; ++k) at[k] = ring + (us + k * slot >= ring_bytes ? us + k * slot - ring_bytes : us + k * slot);
+    Eight x[K][NV];              // 0 past the row's end
     if (RES) {
       float m[K], s[K];
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          if (k < n) sy.get(x[k][i], at[k], r + k, i, dim);
+          if (k < n) sy.get(x[k][i], at[k], k * a.y_stride, i, dim);
           else x[k][i].fill(0.f);
         }
-      if (a.post_norm != kNone) {
+      if (POST == 2 ? a.post_norm != kNone : POST == 1) {
         row_stats<P, NV, K>(x, a.post_norm, a.post_eps, dim, sh, half, nwarps, m, s);
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -113,28 +122,28 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           Eight v;
-          sx.get(v, at[k], r + k, i, dim);
+          sx.get(v, at[k], k * a.x_stride, i, dim);
 #pragma unroll
           for (int q = 0; q < 4; ++q) x[k][i].p[q] = fma(gate[i].p[q], x[k][i].p[q], v.p[q]);
-          store8<P>(static_cast<XT*>(a.x_out) + (r + k) * a.x_out_stride, x[k][i], i, dim);
-          if (NORM) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) x[k][i].p[q] = present<P>(x[k][i].p[q], i, q, dim);
-          }
+          store8<P>(xo, x[k][i], i, dim);
         }
+        xo += a.x_out_stride;
       }
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          if (k < n) sx.get(x[k][i], at[k], r + k, i, dim);
+          if (k < n) sx.get(x[k][i], at[k], k * a.x_stride, i, dim);
           else x[k][i].fill(0.f);
         }
     }
     if (RING) {                 // everything of these rows is in registers: their slots are free
       for (int k = 0; k < n; ++k) fetch();
-      us = us + n >= depth ? us + n - depth : us + n;
+      us = us + n * slot >= ring_bytes ? us + n * slot - ring_bytes : us + n * slot;
+    } else {
+      sx.p += n * a.x_stride;
+      if (RES) sy.p += n * a.y_stride;
     }
     if (NORM) {
       float m[K], s[K];
@@ -147,20 +156,22 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             x[k][i].p[q] = fma(mul(add(x[k][i].p[q], both(-m[k])), both(s[k])), times[i].p[q], plus[i].p[q]);
-          store8<P>(static_cast<BT*>(a.h) + (r + k) * a.h_stride, x[k][i], i, dim);
+          store8<P>(ho, x[k][i], i, dim);
         }
+        ho += a.h_stride;
       }
     }
-    r += n;
+    left -= n;
+    of_group -= n;
   }
   if (RING) wait_async<0>();
 }
 
 // ----------------------------------------------------------------- launch --
-template <typename XT, typename BT, int P, bool RING, int NV, bool RES, bool NORM>
+template <typename XT, typename BT, int P, bool RING, int NV, bool RES, bool NORM, int POST>
 cudaError_t run(const RowArgs& a, cudaStream_t s) {
-  constexpr int K = NV == 1 ? 4 : (NV == 2 ? 2 : 1);
-  const auto kernel = row_fwd_kernel<XT, BT, P, RING, NV, K, RES, NORM>;
+  constexpr int K = NV == 1 ? (POST == 1 ? 2 : 4) : (NV == 2 ? 2 : 1);
+  const auto kernel = row_fwd_kernel<XT, BT, P, RING, NV, K, RES, NORM, POST>;
   const int threads = row_threads(a.dim, NV);
   // blocks of an SM: by registers (96 a thread), then the ring takes what shared memory is left
   int blocks = 640 / threads < 16 ? 640 / threads : 16;
@@ -187,9 +198,11 @@ cudaError_t run(const RowArgs& a, cudaStream_t s) {
 
 template <typename XT, typename BT, int P, bool RING, int NV>
 cudaError_t by_op(const RowArgs& a, cudaStream_t s) {
-  if (a.y && a.h) return run<XT, BT, P, RING, NV, true, true>(a, s);
-  if (a.y) return run<XT, BT, P, RING, NV, true, false>(a, s);
-  return run<XT, BT, P, RING, NV, false, true>(a, s);
+  if (a.y && a.h)
+    return a.post_norm == kNone ? run<XT, BT, P, RING, NV, true, true, 0>(a, s)
+                                : run<XT, BT, P, RING, NV, true, true, 1>(a, s);
+  if (a.y) return run<XT, BT, P, RING, NV, true, false, 2>(a, s);
+  return run<XT, BT, P, RING, NV, false, true, 0>(a, s);
 }
 
 // Rows above 8192 elements are read where they are used.

@@ -75,22 +75,24 @@ __device__ __forceinline__ float2 present(float2 v, int i, int q, int dim) {
   return make_float2(column<P>(i, 2 * q) < dim ? v.x : 0.f, column<P>(i, 2 * q + 1) < dim ? v.y : 0.f);
 }
 
-// One operand of the ring: its place in a slot, and where its rows come from.
+// A row operand: the next row to copy (RING) or to read, and the operand's
+// place in a slot of the ring.
 template <typename T, int P, bool RING, int NV>
 struct Stream {
-  const T* base;
-  long long stride;
+  const T* p;
   uint32_t at;       // bytes into a slot
 
-  __device__ __forceinline__ void fetch(uint32_t slot, long long r, int dim) const {
+  __device__ __forceinline__ void seek(const void* base, long long stride, long long r) {
+    p = static_cast<const T*>(base) + r * stride;
+  }
+  __device__ __forceinline__ void fetch(uint32_t slot, int dim) const {
     if constexpr (RING) {
-      const T* row = base + r * stride;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < 8; e += P) {
           const int c = column<P>(i, e);
-          if (c < dim) copy_async<P * (int)sizeof(T)>(slot + at + c * (int)sizeof(T), row + c);
+          if (c < dim) copy_async<P * (int)sizeof(T)>(slot + at + c * (int)sizeof(T), p + c);
         }
     }
   }
@@ -104,13 +106,14 @@ struct Stream {
         if (c >= dim) reinterpret_cast<T*>(slot + at)[c] = T(0.f);
       }
   }
-  __device__ __forceinline__ void get(Eight& v, const unsigned char* slot, long long r, int i, int dim) const {
+  // The row in a slot, or `ahead` elements past the next one in memory.
+  __device__ __forceinline__ void get(Eight& v, const unsigned char* slot, long long ahead, int i, int dim) const {
     if constexpr (RING) {
       const T* row = reinterpret_cast<const T*>(slot + at);
 #pragma unroll
       for (int e = 0; e < 8; e += P) load_piece<T, P>(v.f() + e, row + column<P>(i, e));
     } else {
-      load8<P>(v, base + r * stride, i, dim);
+      load8<P>(v, p + ahead, i, dim);
     }
   }
 };
@@ -118,12 +121,12 @@ struct Stream {
 // The bytes an operand takes in a slot.
 __host__ __device__ inline uint32_t slot_bytes(int threads, int nv, int elem) { return (uint32_t)(threads * nv * 8 * elem); }
 
-template <int K>
+// Scratch of the sums of N values at once, and the columns that each warp owns.
+template <int N>
 struct Shared {
-  Scratch<2 * K> sums;
-  float count[32];     // columns each warp owns
+  Scratch<N> sums;
+  float count[32];
 };
-
 template <int P, int NV>
 __device__ __forceinline__ void count_columns(float* count, int dim) {
   float c[1] = {0.f};
@@ -140,8 +143,8 @@ __device__ __forceinline__ void count_columns(float* count, int dim) {
 // registers.  The layer norm's second moment is taken about each warp's own
 // mean and the warps' moments are merged (Chan, Golub and LeVeque, 1979), so
 // a row far from zero loses nothing and one barrier is enough.
-template <int P, int NV, int K>
-__device__ __forceinline__ void row_stats(const Eight (&v)[K][NV], int kind, float eps, int dim, Shared<K>& sh,
+template <int P, int NV, int K, int S>
+__device__ __forceinline__ void row_stats(const Eight (&v)[K][NV], int kind, float eps, int dim, Shared<S>& sh,
                                           int& half, int nwarps, float (&mean)[K], float (&rstd)[K]) {
   const float inv_dim = 1.f / (float)dim;
   float s[K];
@@ -197,20 +200,18 @@ __device__ __forceinline__ void row_stats(const Eight (&v)[K][NV], int kind, flo
     if (sub == 0) b[warp] = make_float2(own, q);
     __syncthreads();
     float2 p[W];
-    float total = 0.f;
+    float cw[W], total = 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       const int w = sub + j * L;
       p[j] = w < nwarps ? b[w] : make_float2(0.f, 0.f);
-      if (w < nwarps) total += sh.count[w] * p[j].x;
+      cw[j] = w < nwarps ? sh.count[w] : 0.f;
+      total += cw[j] * p[j].x;
     }
     mu = spread_sum<K>(total) * inv_dim;
     q = 0.f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      const int w = sub + j * L;
-      if (w < nwarps) q += p[j].y + sh.count[w] * (p[j].x - mu) * (p[j].x - mu);
-    }
+    for (int j = 0; j < W; ++j) q += p[j].y + cw[j] * (p[j].x - mu) * (p[j].x - mu);
     q = spread_sum<K>(q);
     half ^= 1;
   }
@@ -221,9 +222,9 @@ __device__ __forceinline__ void row_stats(const Eight (&v)[K][NV], int kind, flo
 // The statistics of K rows x' and, for the gradient u that reaches their norm,
 // mean(u) (0 for the rms norm) and mean(u xhat), with one barrier: the sums
 // with u are taken about the warps' means as well and merged alike.
-template <int P, int NV, int K>
+template <int P, int NV, int K, int S>
 __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][NV], const Eight (&u)[K][NV], int kind, float eps,
-                                              int dim, Shared<K>& sh, int& half, int nwarps, float (&mean)[K],
+                                              int dim, Shared<S>& sh, int& half, int nwarps, float (&mean)[K],
                                               float (&rstd)[K], float (&mu0)[K], float (&mu1)[K]) {
   const float inv_dim = 1.f / (float)dim;
   float s[2 * K];
@@ -254,7 +255,7 @@ __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][NV], const Eig
   // the sum of u (x' - its mean)
   constexpr int N = 2 * K, L = 32 / N, W = (32 + L - 1) / L;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
-  const float n = sh.count[warp], inv_n = n > 0.f ? 1.f / n : 0.f;
+  const float inv_n = sh.count[warp] > 0.f ? 1.f / sh.count[warp] : 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float2 t0 = both(0.f), t1 = both(0.f);
@@ -294,14 +295,14 @@ __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][NV], const Eig
     __syncthreads();
     const float2* bx = sh.sums.v[half] + ((lane & 15) / L) * 33;     // x' of the row this lane stands for
     float2 p[W];
-    float xm[W];
-    float total = 0.f;
+    float xm[W], cw[W], total = 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       const int w = sub + j * L;
       p[j] = w < nwarps ? b[w] : make_float2(0.f, 0.f);
       xm[j] = w < nwarps ? bx[w].x : 0.f;
-      if (w < nwarps) total += lane < 16 ? sh.count[w] * p[j].x : p[j].x;
+      cw[j] = w < nwarps ? sh.count[w] : 0.f;
+      total += (lane < 16 ? cw[j] : 1.f) * p[j].x;
     }
     mu = spread_sum<N>(total);
     if (lane < 16) mu *= inv_dim;
@@ -309,9 +310,8 @@ __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][NV], const Eig
     second = 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const int w = sub + j * L;
       const float off = xm[j] - mx;
-      if (w < nwarps) second += p[j].y + off * (lane < 16 ? sh.count[w] * off : p[j].x);
+      second += p[j].y + off * (lane < 16 ? cw[j] * off : p[j].x);
     }
     second = spread_sum<N>(second);
     half ^= 1;

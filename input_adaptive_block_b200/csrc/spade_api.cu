@@ -336,7 +336,7 @@ cudaError_t host_pipe_setup(HostPipe& P, size_t n_events) {
 
 // ---- row passes around the attention: checks of their operands ----
 
-constexpr long long kMaxRows = 1LL << 40;
+constexpr long long kMaxRows = 1LL << 37;     // a block's share of them is counted in 31 bits
 
 // A list of rows in memory, for the overlap checks (bytes).
 struct Region {
