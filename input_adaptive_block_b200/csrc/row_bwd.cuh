@@ -49,16 +49,18 @@ struct Run {
 // the weights' sums are added up over the block's units in `part`
 // [block][3][dim].
 // POST: the branch has a norm (0 no, 1 yes, 2 as the call says).
-template <typename XT, typename BT, int P, bool RING, int NV, int K, bool RES, bool NORM, int POST>
-__global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
+template <typename XT, typename BT, class L, int K, bool RES, bool NORM, int POST>
+__global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1)
     row_bwd_kernel(const __grid_constant__ RowArgs a, int depth, bool weights) {
+  constexpr int NV = L::NV;
+  constexpr bool RING = L::RING;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Shared<2 * K> sh;
   const int dim = a.dim, nwarps = blockDim.x >> 5;
   const bool post = RES && (POST == 2 ? a.post_norm != kNone : POST == 1), grad = a.dx_out != nullptr;
   const uint32_t xb = slot_bytes(blockDim.x, NV, sizeof(XT)), bb = slot_bytes(blockDim.x, NV, sizeof(BT));
-  Stream<XT, P, RING, NV> sg, sx;
-  Stream<BT, P, RING, NV> sy, sd;
+  Stream<XT, L> sg, sx;
+  Stream<BT, L> sy, sd;
   sg.at = 0;
   sy.at = xb;
   sx.at = xb + (RES ? bb : 0);
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
       fetch();
     }
   }
-  count_columns<P, NV>(sh.count, dim);
+  count_columns<L>(sh.count, dim);
   int half = 0;
   bool first = true;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
@@ -140,15 +142,15 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
     for (int i = 0; i < NV; ++i) {
       Eight t;
       if (RES) {
-        load_param<P>(gate[i], a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
-        load_param<P>(t, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
+        load_param<L>(gate[i], a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
+        load_param<L>(t, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          gate[i].p[q] = present<P>(mul(gate[i].p[q], mul(both(a.residual_scale), t.p[q])), i, q, dim);
+          gate[i].p[q] = present<L>(mul(gate[i].p[q], mul(both(a.residual_scale), t.p[q])), i, q, dim);
       }
       if (NORM) {
-        load_param<P>(times[i], a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
-        load_param<P>(t, a.weight, 0, a.param_bf16, 1.f, i, dim);
+        load_param<L>(times[i], a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
+        load_param<L>(t, a.weight, 0, a.param_bf16, 1.f, i, dim);
 #pragma unroll
         for (int q = 0; q < 4; ++q) times[i].p[q] = mul(add(both(1.f), times[i].p[q]), t.p[q]);
       }
@@ -157,15 +159,21 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
       C[i].fill(0.f);
     }
     for (int left = run.rows; left > 0;) {
+      // K rows at once; where fewer are left, the first stands in for the others,
+      // which are neither added up nor written
       const int n = left < K ? left : K;
+      auto at_row = [&](int k) { return k < n ? k : 0; };
       if (RING) wait_async_upto(depth - K);
       const unsigned char* at[K];
 #pragma unroll
-      for (int k = 0; k < K; ++k) at[k] = ring + (us + k * slot >= ring_bytes ? us + k * slot - ring_bytes : us + k * slot);
+      for (int k = 0; k < K; ++k) {
+        const uint32_t s = us + at_row(k) * slot;
+        at[k] = ring + (s >= ring_bytes ? s - ring_bytes : s);
+      }
       Eight v[K][NV];                  // x', then the gradient that reaches P (0 past the row's end)
       float ym[K], ys[K];
       auto get_yhat = [&](Eight& y, int k, int i) {
-        sy.get(y, at[k], k * a.y_stride, i, dim);
+        sy.get(y, at[k], at_row(k) * a.y_stride, i, dim);
         if (post) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) y.p[q] = mul(add(y.p[q], both(-ym[k])), both(ys[k]));
@@ -175,11 +183,8 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            if (k < n) sy.get(v[k][i], at[k], k * a.y_stride, i, dim);
-            else v[k][i].fill(0.f);
-          }
-        row_stats<P, NV, K>(v, a.post_norm, a.post_eps, dim, sh, half, nwarps, ym, ys);
+          for (int i = 0; i < NV; ++i) sy.get(v[k][i], at[k], at_row(k) * a.y_stride, i, dim);
+        row_stats<L, K>(v, a.post_norm, a.post_eps, dim, sh, half, nwarps, ym, ys);
       }
       float xm[K], xs[K], m0[K], m1[K];
       if (NORM) {
@@ -188,23 +193,18 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
         for (int k = 0; k < K; ++k)
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
-            if (k < n) {
-              sx.get(v[k][i], at[k], k * a.x_stride, i, dim);
-              if (RES) {
-                Eight y;
-                get_yhat(y, k, i);
+            sx.get(v[k][i], at[k], at_row(k) * a.x_stride, i, dim);
+            if (RES) {
+              Eight y;
+              get_yhat(y, k, i);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[k][i].p[q] = fma(gate[i].p[q], y.p[q], v[k][i].p[q]);
-              }
-              sd.get(w[k][i], at[k], k * a.dh_stride, i, dim);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) w[k][i].p[q] = mul(w[k][i].p[q], times[i].p[q]);
-            } else {
-              v[k][i].fill(0.f);
-              w[k][i].fill(0.f);
+              for (int q = 0; q < 4; ++q) v[k][i].p[q] = fma(gate[i].p[q], y.p[q], v[k][i].p[q]);
             }
+            sd.get(w[k][i], at[k], at_row(k) * a.dh_stride, i, dim);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[k][i].p[q] = mul(w[k][i].p[q], times[i].p[q]);
           }
-        row_stats_bwd<P, NV, K>(v, w, a.norm, a.eps, dim, sh, half, nwarps, xm, xs, m0, m1);
+        row_stats_bwd<L, K>(v, w, a.norm, a.eps, dim, sh, half, nwarps, xm, xs, m0, m1);
       }
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -212,11 +212,11 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           Eight gr;
-          if (grad) sg.get(gr, at[k], k * a.dx_out_stride, i, dim);
+          if (grad) sg.get(gr, at[k], at_row(k) * a.dx_out_stride, i, dim);
           else gr.fill(0.f);
           if (NORM) {
             Eight dh;
-            sd.get(dh, at[k], k * a.dh_stride, i, dim);
+            sd.get(dh, at[k], at_row(k) * a.dh_stride, i, dim);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float2 xh = mul(add(v[k][i].p[q], both(-xm[k])), both(xs[k]));
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
               const float2 u = fma(dh.p[q], times[i].p[q], both(-m0[k]));
               gr.p[q] = fma(both(xs[k]), fma(xh, both(-m1[k]), u), gr.p[q]);
             }
-            store8<P>(dxo + k * a.dx_stride, gr, i, dim);
+            store8<L>(dxo + k * a.dx_stride, gr, i, dim);
           }
           if (RES) {
             Eight y;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
               C[i].p[q] = fma(gr.p[q], y.p[q], C[i].p[q]);
               v[k][i].p[q] = mul(gr.p[q], gate[i].p[q]);
             }
-            if (!post) store8<P>(dyo + k * a.dy_stride, v[k][i], i, dim);
+            if (!post) store8<L>(dyo + k * a.dy_stride, v[k][i], i, dim);
           }
         }
       }
@@ -244,16 +244,14 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           float2 t0 = both(0.f), t1 = both(0.f);
-          if (k < n) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-              Eight y;
-              get_yhat(y, k, i);
+          for (int i = 0; i < NV; ++i) {
+            Eight y;
+            get_yhat(y, k, i);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                t0 = add(t0, v[k][i].p[q]);
-                t1 = fma(v[k][i].p[q], y.p[q], t1);
-              }
+            for (int q = 0; q < 4; ++q) {
+              t0 = add(t0, v[k][i].p[q]);
+              t1 = fma(v[k][i].p[q], y.p[q], t1);
             }
           }
           t[k] = sum_of(t0);
@@ -272,12 +270,14 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               y.p[q] = mul(both(ys[k]), fma(y.p[q], both(-p1), add(v[k][i].p[q], both(-p0))));
-            store8<P>(dyo + k * a.dy_stride, y, i, dim);
+            store8<L>(dyo + k * a.dy_stride, y, i, dim);
           }
         }
       }
       if (RING) {
-        for (int k = 0; k < n; ++k) fetch();
+        #pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (k < n) fetch();
         us = us + n * slot >= ring_bytes ? us + n * slot - ring_bytes : us + n * slot;
       } else {
         advance(n);
@@ -291,10 +291,10 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (NORM) {
-          store8<P>(p, A[i], i, dim);
-          store8<P>(p + dim, B[i], i, dim);
+          store8<L>(p, A[i], i, dim);
+          store8<L>(p + dim, B[i], i, dim);
         }
-        if (RES) store8<P>(p + 2 * (long long)dim, C[i], i, dim);
+        if (RES) store8<L>(p + 2 * (long long)dim, C[i], i, dim);
       }
       continue;
     }
@@ -302,25 +302,25 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
     auto add_up = [&](float* to, const Eight& t, int i) {       // columns of this thread alone
       Eight s;
       if (first) s.fill(0.f);
-      else load8<P>(s, to, i, dim);
+      else load8<L>(s, to, i, dim);
 #pragma unroll
       for (int q = 0; q < 4; ++q) s.p[q] = add(s.p[q], t.p[q]);
-      store8<P>(to, s, i, dim);
+      store8<L>(to, s, i, dim);
     };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       Eight t, w, b;
       if (NORM) {
-        load_param<P>(w, a.weight, 0, a.param_bf16, 1.f, i, dim);
-        load_param<P>(b, a.bias, 0, a.param_bf16, 0.f, i, dim);
-        if (a.dshift) store8<P>(a.dshift + g * dim, A[i], i, dim);
+        load_param<L>(w, a.weight, 0, a.param_bf16, 1.f, i, dim);
+        load_param<L>(b, a.bias, 0, a.param_bf16, 0.f, i, dim);
+        if (a.dshift) store8<L>(a.dshift + g * dim, A[i], i, dim);
         if (a.dscale) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) t.p[q] = fma(w.p[q], B[i].p[q], mul(b.p[q], A[i].p[q]));
-          store8<P>(a.dscale + g * dim, t, i, dim);
+          store8<L>(a.dscale + g * dim, t, i, dim);
         }
         if (weights) {
-          load_param<P>(b, a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
+          load_param<L>(b, a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
 #pragma unroll
           for (int q = 0; q < 4; ++q) t.p[q] = mul(add(both(1.f), b.p[q]), A[i].p[q]);
           add_up(p, t, i);
@@ -330,14 +330,14 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
         }
       }
       if (RES) {
-        load_param<P>(w, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
+        load_param<L>(w, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
         if (a.dgate) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) t.p[q] = mul(mul(both(a.residual_scale), w.p[q]), C[i].p[q]);
-          store8<P>(a.dgate + g * dim, t, i, dim);
+          store8<L>(a.dgate + g * dim, t, i, dim);
         }
         if (weights) {
-          load_param<P>(b, a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
+          load_param<L>(b, a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
 #pragma unroll
           for (int q = 0; q < 4; ++q) t.p[q] = mul(mul(both(a.residual_scale), b.p[q]), C[i].p[q]);
           add_up(p + 2 * (long long)dim, t, i);
@@ -350,15 +350,15 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1)
 }
 
 // ----------------------------------------------------------------- launch --
-template <typename XT, typename BT, int P, bool RING, int NV, bool RES, bool NORM, int POST>
+template <typename XT, typename BT, class L, bool RES, bool NORM, int POST>
 cudaError_t run(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
-  constexpr int K = NV == 1 && POST != 1 ? 2 : 1;
-  const int threads = row_threads(a.dim, NV);
-  const size_t slot = slot_bytes(threads, NV, sizeof(XT)) * (NORM ? 2 : 1) +
-                      slot_bytes(threads, NV, sizeof(BT)) * ((RES ? 1 : 0) + (NORM ? 1 : 0));
+  constexpr int K = L::NV == 1 && POST != 1 ? 2 : 1;
+  const int threads = row_threads(a.dim, L::NV);
+  const size_t slot = slot_bytes(threads, L::NV, sizeof(XT)) * (NORM ? 2 : 1) +
+                      slot_bytes(threads, L::NV, sizeof(BT)) * ((RES ? 1 : 0) + (NORM ? 1 : 0));
   int depth = 0;
   size_t smem = 0;
-  if (RING) {
+  if (L::RING) {
     const size_t room = kSmemSm / bwd_blocks(a.dim) - 1024 - sizeof(Shared<2 * K>);
     const long long rows = (a.rows + grid - 1) / grid;
     depth = (int)(room / slot < kDepthMax ? room / slot : kDepthMax);
@@ -366,7 +366,7 @@ cudaError_t run(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
     if (depth < K) return cudaErrorInvalidConfiguration;
     smem = depth * slot;
   }
-  const auto kernel = row_bwd_kernel<XT, BT, P, RING, NV, K, RES, NORM, POST>;
+  const auto kernel = row_bwd_kernel<XT, BT, L, K, RES, NORM, POST>;
   if (smem > 32 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -375,37 +375,40 @@ cudaError_t run(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename XT, typename BT, int P, bool RING, int NV>
+template <typename XT, typename BT, class L>
 cudaError_t by_op(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
   if (a.dy && a.dh)
-    return a.post_norm == kNone ? run<XT, BT, P, RING, NV, true, true, 0>(a, grid, weights, s)
-                                : run<XT, BT, P, RING, NV, true, true, 1>(a, grid, weights, s);
-  if (a.dy) return run<XT, BT, P, RING, NV, true, false, 2>(a, grid, weights, s);
-  return run<XT, BT, P, RING, NV, false, true, 0>(a, grid, weights, s);
+    return a.post_norm == kNone ? run<XT, BT, L, true, true, 0>(a, grid, weights, s)
+                                : run<XT, BT, L, true, true, 1>(a, grid, weights, s);
+  if (a.dy) return run<XT, BT, L, true, false, 2>(a, grid, weights, s);
+  return run<XT, BT, L, false, true, 0>(a, grid, weights, s);
 }
 
-// Rows above 8192 elements are read where they are used.
-template <typename XT, typename BT, int P, bool RING>
+// The widest pieces have kernels for every length; rows above 8192 elements,
+// and rows above 5120 in narrower pieces, are read where they are used.
+template <typename XT, typename BT>
 cudaError_t by_width(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
-  switch (row_nv(a.dim)) {
-    case 1: return by_op<XT, BT, P, RING, 1>(a, grid, weights, s);
-    case 2: return by_op<XT, BT, P, RING, 2>(a, grid, weights, s);
-    default: return by_op<XT, BT, P == 2 ? 1 : P, false, 4>(a, grid, weights, s);
+  constexpr int P = sizeof(XT) == 2 ? 8 : 4;
+  const int p = piece_of(a);
+  const bool wide = p == P;
+  if (a.dim <= 5120) {
+    const bool full = a.dim % 256 == 0;
+    if (wide) return full ? by_op<XT, BT, Layout<P, true, true, 1>>(a, grid, weights, s) : by_op<XT, BT, Layout<P, false, true, 1>>(a, grid, weights, s);
+    if constexpr (sizeof(XT) == 2) {
+      if (p > 1) return by_op<XT, BT, Layout<2, false, true, 1>>(a, grid, weights, s);
+    }
+    return by_op<XT, BT, Layout<1, false, sizeof(BT) == 4, 1>>(a, grid, weights, s);
   }
+  if (a.dim <= 8192 && wide)
+    return a.dim % 512 == 0 ? by_op<XT, BT, Layout<P, true, true, 2>>(a, grid, weights, s) : by_op<XT, BT, Layout<P, false, true, 2>>(a, grid, weights, s);
+  return wide ? by_op<XT, BT, Layout<P, false, false, 4>>(a, grid, weights, s) : by_op<XT, BT, Layout<1, false, false, 4>>(a, grid, weights, s);
 }
 
 }  // namespace
 
 template <typename XT, typename BT>
 cudaError_t row_bwd(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
-  const int p = piece_of(a);
-  if constexpr (sizeof(XT) == 2) {
-    if (p == 8) return by_width<XT, BT, 8, true>(a, grid, weights, s);
-    return p > 1 ? by_width<XT, BT, 2, true>(a, grid, weights, s) : by_width<XT, BT, 1, false>(a, grid, weights, s);
-  } else {
-    return p == 4 ? by_width<XT, BT, 4, true>(a, grid, weights, s)
-                  : by_width<XT, BT, 1, sizeof(BT) == 4>(a, grid, weights, s);
-  }
+  return by_width<XT, BT>(a, grid, weights, s);
 }
 
 }  // namespace spade

@@ -17,14 +17,16 @@ namespace {
 using namespace rowpass;
 
 // POST: the branch has a norm (0 no, 1 yes, 2 as the call says).
-template <typename XT, typename BT, int P, bool RING, int NV, int K, bool RES, bool NORM, int POST>
-__global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const __grid_constant__ RowArgs a, int depth) {
+template <typename XT, typename BT, class L, int K, bool RES, bool NORM, int POST>
+__global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1) row_fwd_kernel(const __grid_constant__ RowArgs a, int depth) {
+  constexpr int NV = L::NV;
+  constexpr bool RING = L::RING;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Shared<K> sh;
   const int dim = a.dim, nwarps = blockDim.x >> 5;
   const long long r0 = a.rows * blockIdx.x / gridDim.x, r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
-  Stream<XT, P, RING, NV> sx;
-  Stream<BT, P, RING, NV> sy;
+  Stream<XT, L> sx;
+  Stream<BT, L> sy;
   sx.seek(a.x, a.x_stride, r0);
   sx.at = 0;
   sy.at = slot_bytes(blockDim.x, NV, sizeof(XT));
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
       fetch();
     }
   }
-  count_columns<P, NV>(sh.count, dim);
+  count_columns<L>(sh.count, dim);
   int half = 0;
   long long g = r0 / a.rows_per_group - 1;
   int of_group = 0;              // rows until the next modulation group
@@ -70,19 +72,19 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
       for (int i = 0; i < NV; ++i) {
         if (RES) {
           Eight pw;
-          load_param<P>(gate[i], a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
-          load_param<P>(pw, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
+          load_param<L>(gate[i], a.gate, g * a.gate_stride, a.param_bf16, 1.f, i, dim);
+          load_param<L>(pw, a.post_weight, 0, a.param_bf16, 1.f, i, dim);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            gate[i].p[q] = present<P>(mul(gate[i].p[q], mul(both(a.residual_scale), pw.p[q])), i, q, dim);
+            gate[i].p[q] = present<L>(mul(gate[i].p[q], mul(both(a.residual_scale), pw.p[q])), i, q, dim);
         }
         if (NORM) {
           // (n w + b)(1 + s) + t = n (w (1 + s)) + (b (1 + s) + t)
           Eight w, b;
-          load_param<P>(times[i], a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
-          load_param<P>(plus[i], a.shift, g * a.shift_stride, a.param_bf16, 0.f, i, dim);
-          load_param<P>(w, a.weight, 0, a.param_bf16, 1.f, i, dim);
-          load_param<P>(b, a.bias, 0, a.param_bf16, 0.f, i, dim);
+          load_param<L>(times[i], a.scale, g * a.scale_stride, a.param_bf16, 0.f, i, dim);
+          load_param<L>(plus[i], a.shift, g * a.shift_stride, a.param_bf16, 0.f, i, dim);
+          load_param<L>(w, a.weight, 0, a.param_bf16, 1.f, i, dim);
+          load_param<L>(b, a.bias, 0, a.param_bf16, 0.f, i, dim);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float2 s1 = add(both(1.f), times[i].p[q]);
@@ -92,74 +94,80 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
         }
       }
     }
+    // N rows of one group at once
+    auto rows = [&](auto count) {
+      constexpr int N = decltype(count)::value;
+      const unsigned char* at[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) at[k] = ring + (us + k * slot >= ring_bytes ? us + k * slot - ring_bytes : us + k * slot);
+      Eight x[N][NV];              // 0 past the row's end
+      if (RES) {
+        float m[N], s[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            sy.get(x[k][i], at[k], k * a.y_stride, i, dim);
+          }
+        if (POST == 2 ? a.post_norm != kNone : POST == 1) {
+          row_stats<L, N>(x, a.post_norm, a.post_eps, dim, sh, half, nwarps, m, s);
+#pragma unroll
+          for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) x[k][i].p[q] = mul(add(x[k][i].p[q], both(-m[k])), both(s[k]));
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            Eight v;
+            sx.get(v, at[k], k * a.x_stride, i, dim);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[k][i].p[q] = fma(gate[i].p[q], x[k][i].p[q], v.p[q]);
+            store8<L>(xo, x[k][i], i, dim);
+          }
+          xo += a.x_out_stride;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            sx.get(x[k][i], at[k], k * a.x_stride, i, dim);
+          }
+      }
+      if (RING) {                 // everything of these rows is in registers: their slots are free
+        #pragma unroll
+        for (int k = 0; k < N; ++k) fetch();
+        us = us + N * slot >= ring_bytes ? us + N * slot - ring_bytes : us + N * slot;
+      } else {
+        sx.p += N * a.x_stride;
+        if (RES) sy.p += N * a.y_stride;
+      }
+      if (NORM) {
+        float m[N], s[N];
+        row_stats<L, N>(x, a.norm, a.eps, dim, sh, half, nwarps, m, s);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              x[k][i].p[q] = fma(mul(add(x[k][i].p[q], both(-m[k])), both(s[k])), times[i].p[q], plus[i].p[q]);
+            store8<L>(ho, x[k][i], i, dim);
+          }
+          ho += a.h_stride;
+        }
+      }
+    };
     const int n = of_group < K ? of_group : K;
     if (RING) wait_async_upto(depth - K);
-    const unsigned char* at[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) at[k] = ring + (us + k * slot >= ring_bytes ? us + k * slot - ring_bytes : us + k * slot);
-    Eight x[K][NV];              // 0 past the row's end
-    if (RES) {
-      float m[K], s[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          if (k < n) sy.get(x[k][i], at[k], k * a.y_stride, i, dim);
-          else x[k][i].fill(0.f);
-        }
-      if (POST == 2 ? a.post_norm != kNone : POST == 1) {
-        row_stats<P, NV, K>(x, a.post_norm, a.post_eps, dim, sh, half, nwarps, m, s);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) x[k][i].p[q] = mul(add(x[k][i].p[q], both(-m[k])), both(s[k]));
-      }
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (k >= n) break;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          Eight v;
-          sx.get(v, at[k], k * a.x_stride, i, dim);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) x[k][i].p[q] = fma(gate[i].p[q], x[k][i].p[q], v.p[q]);
-          store8<P>(xo, x[k][i], i, dim);
-        }
-        xo += a.x_out_stride;
-      }
+    if (n == K) {
+      rows(std::integral_constant<int, K>());
     } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          if (k < n) sx.get(x[k][i], at[k], k * a.x_stride, i, dim);
-          else x[k][i].fill(0.f);
-        }
-    }
-    if (RING) {                 // everything of these rows is in registers: their slots are free
-      for (int k = 0; k < n; ++k) fetch();
-      us = us + n * slot >= ring_bytes ? us + n * slot - ring_bytes : us + n * slot;
-    } else {
-      sx.p += n * a.x_stride;
-      if (RES) sy.p += n * a.y_stride;
-    }
-    if (NORM) {
-      float m[K], s[K];
-      row_stats<P, NV, K>(x, a.norm, a.eps, dim, sh, half, nwarps, m, s);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (k >= n) break;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            x[k][i].p[q] = fma(mul(add(x[k][i].p[q], both(-m[k])), both(s[k])), times[i].p[q], plus[i].p[q]);
-          store8<P>(ho, x[k][i], i, dim);
-        }
-        ho += a.h_stride;
-      }
+      for (int k = 0; k < n; ++k) rows(std::integral_constant<int, 1>());
     }
     left -= n;
     of_group -= n;
@@ -168,11 +176,11 @@ __global__ void __launch_bounds__(NV == 1 ? 640 : 512, 1) row_fwd_kernel(const _
 }
 
 // ----------------------------------------------------------------- launch --
-template <typename XT, typename BT, int P, bool RING, int NV, bool RES, bool NORM, int POST>
+template <typename XT, typename BT, class L, bool RES, bool NORM, int POST>
 cudaError_t run(const RowArgs& a, cudaStream_t s) {
-  constexpr int K = NV == 1 ? (POST == 1 ? 2 : 4) : (NV == 2 ? 2 : 1);
-  const auto kernel = row_fwd_kernel<XT, BT, P, RING, NV, K, RES, NORM, POST>;
-  const int threads = row_threads(a.dim, NV);
+  constexpr int K = L::NV == 1 ? (POST == 1 ? 2 : 4) : (L::NV == 2 ? 2 : 1);
+  const auto kernel = row_fwd_kernel<XT, BT, L, K, RES, NORM, POST>;
+  const int threads = row_threads(a.dim, L::NV);
   // blocks of an SM: by registers (96 a thread), then the ring takes what shared memory is left
   int blocks = 640 / threads < 16 ? 640 / threads : 16;
   if (blocks < 1) blocks = 1;
@@ -180,8 +188,8 @@ cudaError_t run(const RowArgs& a, cudaStream_t s) {
   const int grid = (int)(a.rows < resident ? a.rows : resident);
   int depth = 0;
   size_t smem = 0;
-  if (RING) {
-    const size_t slot = slot_bytes(threads, NV, sizeof(XT)) + (RES ? slot_bytes(threads, NV, sizeof(BT)) : 0);
+  if (L::RING) {
+    const size_t slot = slot_bytes(threads, L::NV, sizeof(XT)) + (RES ? slot_bytes(threads, L::NV, sizeof(BT)) : 0);
     const size_t room = kSmemSm / blocks - 1024 - sizeof(Shared<K>);
     const long long rows = (a.rows + grid - 1) / grid;
     depth = (int)(room / slot < kDepthMax ? room / slot : kDepthMax);
@@ -196,36 +204,40 @@ cudaError_t run(const RowArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename XT, typename BT, int P, bool RING, int NV>
+template <typename XT, typename BT, class L>
 cudaError_t by_op(const RowArgs& a, cudaStream_t s) {
   if (a.y && a.h)
-    return a.post_norm == kNone ? run<XT, BT, P, RING, NV, true, true, 0>(a, s)
-                                : run<XT, BT, P, RING, NV, true, true, 1>(a, s);
-  if (a.y) return run<XT, BT, P, RING, NV, true, false, 2>(a, s);
-  return run<XT, BT, P, RING, NV, false, true, 0>(a, s);
+    return a.post_norm == kNone ? run<XT, BT, L, true, true, 0>(a, s)
+                                : run<XT, BT, L, true, true, 1>(a, s);
+  if (a.y) return run<XT, BT, L, true, false, 2>(a, s);
+  return run<XT, BT, L, false, true, 0>(a, s);
 }
 
-// Rows above 8192 elements are read where they are used.
-template <typename XT, typename BT, int P, bool RING>
+// The widest pieces have kernels for every length; rows above 8192 elements,
+// and rows above 5120 in narrower pieces, are read where they are used.
+template <typename XT, typename BT>
 cudaError_t by_width(const RowArgs& a, cudaStream_t s) {
-  switch (row_nv(a.dim)) {
-    case 1: return by_op<XT, BT, P, RING, 1>(a, s);
-    case 2: return by_op<XT, BT, P, RING, 2>(a, s);
-    default: return by_op<XT, BT, P == 2 ? 1 : P, false, 4>(a, s);
+  constexpr int P = sizeof(XT) == 2 ? 8 : 4;
+  const int p = piece_of(a);
+  const bool wide = p == P;
+  if (a.dim <= 5120) {
+    const bool full = a.dim % 256 == 0;
+    if (wide) return full ? by_op<XT, BT, Layout<P, true, true, 1>>(a, s) : by_op<XT, BT, Layout<P, false, true, 1>>(a, s);
+    if constexpr (sizeof(XT) == 2) {
+      if (p > 1) return by_op<XT, BT, Layout<2, false, true, 1>>(a, s);
+    }
+    return by_op<XT, BT, Layout<1, false, sizeof(BT) == 4, 1>>(a, s);
   }
+  if (a.dim <= 8192 && wide)
+    return a.dim % 512 == 0 ? by_op<XT, BT, Layout<P, true, true, 2>>(a, s) : by_op<XT, BT, Layout<P, false, true, 2>>(a, s);
+  return wide ? by_op<XT, BT, Layout<P, false, false, 4>>(a, s) : by_op<XT, BT, Layout<1, false, false, 4>>(a, s);
 }
 
 }  // namespace
 
 template <typename XT, typename BT>
 cudaError_t row_fwd(const RowArgs& a, cudaStream_t s) {
-  const int p = piece_of(a);
-  if constexpr (sizeof(XT) == 2) {
-    if (p == 8) return by_width<XT, BT, 8, true>(a, s);
-    return p > 1 ? by_width<XT, BT, 2, true>(a, s) : by_width<XT, BT, 1, false>(a, s);
-  } else {
-    return p == 4 ? by_width<XT, BT, 4, true>(a, s) : by_width<XT, BT, 1, sizeof(BT) == 4>(a, s);
-  }
+  return by_width<XT, BT>(a, s);
 }
 
 }  // namespace spade

@@ -22,9 +22,21 @@ using namespace rowio;
 
 enum { kNone = SPADE_NORM_NONE, kRms = SPADE_NORM_RMS, kLayer = SPADE_NORM_LAYER };
 
-template <int P>
+// FULL: the threads' columns are exactly the row's.
+template <int P_, bool FULL_, bool RING_, int NV_>
+struct Layout {
+  static constexpr int P = P_, NV = NV_;
+  static constexpr bool FULL = FULL_, RING = RING_;
+};
+template <class L>
 __device__ __forceinline__ int column(int i, int e) {
+  constexpr int P = L::P;
   return ((i * (8 / P) + e / P) * (int)blockDim.x + (int)threadIdx.x) * P + e % P;
+}
+
+template <class L>
+__device__ __forceinline__ bool inside(int column, int dim) {
+  return L::FULL || column < dim;
 }
 
 // A thread's eight elements, as pairs.
@@ -39,12 +51,13 @@ struct Eight {
   }
 };
 
-template <int P, typename T>
+template <class L, typename T>
 __device__ __forceinline__ void load8(Eight& v, const T* row, int i, int dim) {
+  constexpr int P = L::P;
 #pragma unroll
   for (int e = 0; e < 8; e += P) {
-    const int c = column<P>(i, e);
-    if (c < dim) {
+    const int c = column<L>(i, e);
+    if (inside<L>(c, dim)) {
       load_piece<T, P>(v.f() + e, row + c);
     } else {
 #pragma unroll
@@ -52,33 +65,36 @@ __device__ __forceinline__ void load8(Eight& v, const T* row, int i, int dim) {
     }
   }
 }
-template <int P, typename T>
+template <class L, typename T>
 __device__ __forceinline__ void store8(T* row, const Eight& v, int i, int dim) {
+  constexpr int P = L::P;
 #pragma unroll
   for (int e = 0; e < 8; e += P) {
-    const int c = column<P>(i, e);
-    if (c < dim) store_piece<P>(row + c, v.f() + e);
+    const int c = column<L>(i, e);
+    if (inside<L>(c, dim)) store_piece<P>(row + c, v.f() + e);
   }
 }
 // A parameter row in either type; absent ones read as `none`.
-template <int P>
+template <class L>
 __device__ __forceinline__ void load_param(Eight& v, const void* p, long long off, bool is_bf16, float none, int i,
                                            int dim) {
   if (!p) v.fill(none);
-  else if (is_bf16) load8<P>(v, static_cast<const bf16*>(p) + off, i, dim);
-  else load8<P>(v, static_cast<const float*>(p) + off, i, dim);
+  else if (is_bf16) load8<L>(v, static_cast<const bf16*>(p) + off, i, dim);
+  else load8<L>(v, static_cast<const float*>(p) + off, i, dim);
 }
 // v in the columns of pair q that the row has, 0 in the others.
-template <int P>
+template <class L>
 __device__ __forceinline__ float2 present(float2 v, int i, int q, int dim) {
-  if (P > 1) return column<P>(i, 2 * q) < dim ? v : both(0.f);
-  return make_float2(column<P>(i, 2 * q) < dim ? v.x : 0.f, column<P>(i, 2 * q + 1) < dim ? v.y : 0.f);
+  if (L::FULL) return v;
+  if (L::P > 1) return column<L>(i, 2 * q) < dim ? v : both(0.f);
+  return make_float2(column<L>(i, 2 * q) < dim ? v.x : 0.f, column<L>(i, 2 * q + 1) < dim ? v.y : 0.f);
 }
 
 // A row operand: the next row to copy (RING) or to read, and the operand's
 // place in a slot of the ring.
-template <typename T, int P, bool RING, int NV>
+template <typename T, class L>
 struct Stream {
+  static constexpr int P = L::P, NV = L::NV;
   const T* p;
   uint32_t at;       // bytes into a slot
 
@@ -86,34 +102,35 @@ struct Stream {
     p = static_cast<const T*>(base) + r * stride;
   }
   __device__ __forceinline__ void fetch(uint32_t slot, int dim) const {
-    if constexpr (RING) {
+    if constexpr (L::RING) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < 8; e += P) {
-          const int c = column<P>(i, e);
-          if (c < dim) copy_async<P * (int)sizeof(T)>(slot + at + c * (int)sizeof(T), p + c);
+          const int c = column<L>(i, e);
+          if (inside<L>(c, dim)) copy_async<P * (int)sizeof(T)>(slot + at + c * (int)sizeof(T), p + c);
         }
     }
   }
   // Columns past the row's end read as zero.
   __device__ __forceinline__ void clear(unsigned char* slot, int dim) const {
+    if (L::FULL) return;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int c = column<P>(i, e);
-        if (c >= dim) reinterpret_cast<T*>(slot + at)[c] = T(0.f);
+        const int c = column<L>(i, e);
+        if (!inside<L>(c, dim)) reinterpret_cast<T*>(slot + at)[c] = T(0.f);
       }
   }
   // The row in a slot, or `ahead` elements past the next one in memory.
   __device__ __forceinline__ void get(Eight& v, const unsigned char* slot, long long ahead, int i, int dim) const {
-    if constexpr (RING) {
+    if constexpr (L::RING) {
       const T* row = reinterpret_cast<const T*>(slot + at);
 #pragma unroll
-      for (int e = 0; e < 8; e += P) load_piece<T, P>(v.f() + e, row + column<P>(i, e));
+      for (int e = 0; e < 8; e += P) load_piece<T, P>(v.f() + e, row + column<L>(i, e));
     } else {
-      load8<P>(v, p + ahead, i, dim);
+      load8<L>(v, p + ahead, i, dim);
     }
   }
 };
@@ -127,13 +144,14 @@ struct Shared {
   Scratch<N> sums;
   float count[32];
 };
-template <int P, int NV>
+template <class L>
 __device__ __forceinline__ void count_columns(float* count, int dim) {
+  constexpr int NV = L::NV;
   float c[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[0] += column<P>(i, e) < dim ? 1.f : 0.f;
+    for (int e = 0; e < 8; ++e) c[0] += inside<L>(column<L>(i, e), dim) ? 1.f : 0.f;
   const float s = warp_sum_spread<1>(c);
   if ((threadIdx.x & 31) == 0) count[threadIdx.x >> 5] = s;
   __syncthreads();
@@ -143,9 +161,10 @@ __device__ __forceinline__ void count_columns(float* count, int dim) {
 // registers.  The layer norm's second moment is taken about each warp's own
 // mean and the warps' moments are merged (Chan, Golub and LeVeque, 1979), so
 // a row far from zero loses nothing and one barrier is enough.
-template <int P, int NV, int K, int S>
-__device__ __forceinline__ void row_stats(const Eight (&v)[K][NV], int kind, float eps, int dim, Shared<S>& sh,
+template <class L, int K, int S>
+__device__ __forceinline__ void row_stats(const Eight (&v)[K][L::NV], int kind, float eps, int dim, Shared<S>& sh,
                                           int& half, int nwarps, float (&mean)[K], float (&rstd)[K]) {
+  constexpr int NV = L::NV;
   const float inv_dim = 1.f / (float)dim;
   float s[K];
   if (kind == kRms) {
@@ -166,8 +185,8 @@ __device__ __forceinline__ void row_stats(const Eight (&v)[K][NV], int kind, flo
     }
     return;
   }
-  constexpr int L = 32 / K, W = (32 + L - 1) / L;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
+  constexpr int M = 32 / K, W = (32 + M - 1) / M;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % M;
   const float n = sh.count[warp];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -188,7 +207,7 @@ __device__ __forceinline__ void row_stats(const Eight (&v)[K][NV], int kind, flo
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float2 off = add(v[k][i].p[q], present<P>(both(-m[k]), i, q, dim));
+        const float2 off = add(v[k][i].p[q], present<L>(both(-m[k]), i, q, dim));
         t = fma(off, off, t);
       }
     s[k] = sum_of(t);
@@ -196,14 +215,14 @@ __device__ __forceinline__ void row_stats(const Eight (&v)[K][NV], int kind, flo
   float q = warp_sum_spread<K>(s);
   float mu = own;
   if (nwarps > 1) {
-    float2* b = sh.sums.v[half] + (lane / L) * 33;
+    float2* b = sh.sums.v[half] + (lane / M) * 33;
     if (sub == 0) b[warp] = make_float2(own, q);
     __syncthreads();
     float2 p[W];
     float cw[W], total = 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const int w = sub + j * L;
+      const int w = sub + j * M;
       p[j] = w < nwarps ? b[w] : make_float2(0.f, 0.f);
       cw[j] = w < nwarps ? sh.count[w] : 0.f;
       total += cw[j] * p[j].x;
@@ -222,10 +241,11 @@ __device__ __forceinline__ void row_stats(const Eight (&v)[K][NV], int kind, flo
 // The statistics of K rows x' and, for the gradient u that reaches their norm,
 // mean(u) (0 for the rms norm) and mean(u xhat), with one barrier: the sums
 // with u are taken about the warps' means as well and merged alike.
-template <int P, int NV, int K, int S>
-__device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][NV], const Eight (&u)[K][NV], int kind, float eps,
+template <class L, int K, int S>
+__device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][L::NV], const Eight (&u)[K][L::NV], int kind, float eps,
                                               int dim, Shared<S>& sh, int& half, int nwarps, float (&mean)[K],
                                               float (&rstd)[K], float (&mu0)[K], float (&mu1)[K]) {
+  constexpr int NV = L::NV;
   const float inv_dim = 1.f / (float)dim;
   float s[2 * K];
   if (kind == kRms) {
@@ -253,8 +273,8 @@ __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][NV], const Eig
   }
   // values of a warp: first the sums of x' and u, then the second moment and
   // the sum of u (x' - its mean)
-  constexpr int N = 2 * K, L = 32 / N, W = (32 + L - 1) / L;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
+  constexpr int N = 2 * K, M = 32 / N, W = (32 + M - 1) / M;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % M;
   const float inv_n = sh.count[warp] > 0.f ? 1.f / sh.count[warp] : 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -280,7 +300,7 @@ __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][NV], const Eig
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float2 off = add(v[k][i].p[q], present<P>(both(-m[k]), i, q, dim));
+        const float2 off = add(v[k][i].p[q], present<L>(both(-m[k]), i, q, dim));
         t0 = fma(off, off, t0);
         t1 = fma(u[k][i].p[q], off, t1);
       }
@@ -290,15 +310,15 @@ __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][NV], const Eig
   float second = warp_sum_spread<N>(s);
   float mu = first;
   if (nwarps > 1) {
-    float2* b = sh.sums.v[half] + (lane / L) * 33;
+    float2* b = sh.sums.v[half] + (lane / M) * 33;
     if (sub == 0) b[warp] = make_float2(first, second);
     __syncthreads();
-    const float2* bx = sh.sums.v[half] + ((lane & 15) / L) * 33;     // x' of the row this lane stands for
+    const float2* bx = sh.sums.v[half] + ((lane & 15) / M) * 33;     // x' of the row this lane stands for
     float2 p[W];
     float xm[W], cw[W], total = 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const int w = sub + j * L;
+      const int w = sub + j * M;
       p[j] = w < nwarps ? b[w] : make_float2(0.f, 0.f);
       xm[j] = w < nwarps ? bx[w].x : 0.f;
       cw[j] = w < nwarps ? sh.count[w] : 0.f;
@@ -356,12 +376,12 @@ inline int row_threads(int dim, int nv) {
   const int t = (dim + 8 * nv - 1) / (8 * nv);
   return (t + 31) / 32 * 32;
 }
-inline int row_nv(int dim) { return dim <= 5120 ? 1 : (dim <= 8192 ? 2 : 4); }
 
-// Blocks of an SM, by registers (96 a thread; 128 of the wide rows').
+// Blocks of an SM in a backward pass, by registers: 96 a thread, 128 where a
+// thread holds more than eight columns.
 inline int bwd_blocks(int dim) {
-  const int threads = row_threads(dim, row_nv(dim));
-  const int b = row_nv(dim) > 1 ? 1 : 640 / threads;
+  if (dim > 5120) return 1;
+  const int b = 640 / row_threads(dim, 1);
   return b < 1 ? 1 : (b > 16 ? 16 : b);
 }
 
