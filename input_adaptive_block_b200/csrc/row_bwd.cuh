@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1)
       fetch();
     }
   }
-  count_columns<L>(sh.count, dim);
+  count_columns<L>(sh, dim);
   int half = 0;
   bool first = true;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1)
         for (int k = 0; k < K; ++k)
 #pragma unroll
           for (int i = 0; i < NV; ++i) sy.get(v[k][i], at[k], at_row(k) * a.y_stride, i, dim);
-        row_stats<L, K>(v, a.post_norm, a.post_eps, dim, sh, half, nwarps, ym, ys);
+        row_stats<L, K>(v, a.post_norm, a.post_eps, a.inv_dim, dim, sh, half, nwarps, ym, ys);
       }
       float xm[K], xs[K], m0[K], m1[K];
       if (NORM) {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) w[k][i].p[q] = mul(w[k][i].p[q], times[i].p[q]);
           }
-        row_stats_bwd<L, K>(v, w, a.norm, a.eps, dim, sh, half, nwarps, xm, xs, m0, m1);
+        row_stats_bwd<L, K>(v, w, a.norm, a.eps, a.inv_dim, dim, sh, half, nwarps, xm, xs, m0, m1);
       }
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -258,11 +258,10 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1)
           t[K + k] = sum_of(t1);
         }
         block_sum(t, sh.sums, half, nwarps);
-        const float inv_dim = 1.f / (float)dim;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           if (k >= n) break;
-          const float p0 = a.post_norm == kLayer ? t[k] * inv_dim : 0.f, p1 = t[K + k] * inv_dim;
+          const float p0 = a.post_norm == kLayer ? t[k] * a.inv_dim : 0.f, p1 = t[K + k] * a.inv_dim;
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
             Eight y;

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1) row_fwd_kernel(cons
       fetch();
     }
   }
-  count_columns<L>(sh.count, dim);
+  count_columns<L>(sh, dim);
   int half = 0;
   long long g = r0 / a.rows_per_group - 1;
   int of_group = 0;              // rows until the next modulation group
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1) row_fwd_kernel(cons
             sy.get(x[k][i], at[k], k * a.y_stride, i, dim);
           }
         if (POST == 2 ? a.post_norm != kNone : POST == 1) {
-          row_stats<L, N>(x, a.post_norm, a.post_eps, dim, sh, half, nwarps, m, s);
+          row_stats<L, N>(x, a.post_norm, a.post_eps, a.inv_dim, dim, sh, half, nwarps, m, s);
 #pragma unroll
           for (int k = 0; k < N; ++k)
 #pragma unroll
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1) row_fwd_kernel(cons
       }
       if (NORM) {
         float m[N], s[N];
-        row_stats<L, N>(x, a.norm, a.eps, dim, sh, half, nwarps, m, s);
+        row_stats<L, N>(x, a.norm, a.eps, a.inv_dim, dim, sh, half, nwarps, m, s);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
 #pragma unroll

@@ -138,23 +138,38 @@ struct Stream {
 // The bytes an operand takes in a slot.
 __host__ __device__ inline uint32_t slot_bytes(int threads, int nv, int elem) { return (uint32_t)(threads * nv * 8 * elem); }
 
-// Scratch of the sums of N values at once, and the columns that each warp owns.
+// Scratch of the sums of N values at once, and the columns that each warp owns
+// (0 past the last warp) with the reciprocal.
 template <int N>
 struct Shared {
   Scratch<N> sums;
-  float count[32];
+  float count[32], inv_count[32];
 };
-template <class L>
-__device__ __forceinline__ void count_columns(float* count, int dim) {
-  constexpr int NV = L::NV;
+template <class L, int N>
+__device__ __forceinline__ void count_columns(Shared<N>& sh, int dim) {
   float c[1] = {0.f};
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < L::NV; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) c[0] += inside<L>(column<L>(i, e), dim) ? 1.f : 0.f;
   const float s = warp_sum_spread<1>(c);
-  if ((threadIdx.x & 31) == 0) count[threadIdx.x >> 5] = s;
+  for (int i = threadIdx.x; i < 2 * N * 33; i += blockDim.x) (&sh.sums.v[0][0])[i] = make_float2(0.f, 0.f);
+  if (threadIdx.x < 32) sh.count[threadIdx.x] = sh.inv_count[threadIdx.x] = 0.f;
   __syncthreads();
+  if ((threadIdx.x & 31) == 0 && s > 0.f) {
+    sh.count[threadIdx.x >> 5] = s;
+    sh.inv_count[threadIdx.x >> 5] = 1.f / s;
+  }
+  __syncthreads();
+}
+// The columns of a warp; all own the same in a FULL layout.
+template <class L, int N>
+__device__ __forceinline__ float count_of(const Shared<N>& sh, int warp) {
+  return L::FULL ? 256.f * L::NV : sh.count[warp];
+}
+template <class L, int N>
+__device__ __forceinline__ float inv_count_of(const Shared<N>& sh, int warp) {
+  return L::FULL ? 1.f / (256.f * L::NV) : sh.inv_count[warp];
 }
 
 // Mean (0 for the rms norm) and reciprocal deviation of K rows held in
@@ -162,10 +177,9 @@ __device__ __forceinline__ void count_columns(float* count, int dim) {
 // mean and the warps' moments are merged (Chan, Golub and LeVeque, 1979), so
 // a row far from zero loses nothing and one barrier is enough.
 template <class L, int K, int S>
-__device__ __forceinline__ void row_stats(const Eight (&v)[K][L::NV], int kind, float eps, int dim, Shared<S>& sh,
-                                          int& half, int nwarps, float (&mean)[K], float (&rstd)[K]) {
+__device__ __forceinline__ void row_stats(const Eight (&v)[K][L::NV], int kind, float eps, float inv_dim, int dim,
+                                          Shared<S>& sh, int& half, int nwarps, float (&mean)[K], float (&rstd)[K]) {
   constexpr int NV = L::NV;
-  const float inv_dim = 1.f / (float)dim;
   float s[K];
   if (kind == kRms) {
 #pragma unroll
@@ -187,7 +201,6 @@ __device__ __forceinline__ void row_stats(const Eight (&v)[K][L::NV], int kind, 
   }
   constexpr int M = 32 / K, W = (32 + M - 1) / M;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % M;
-  const float n = sh.count[warp];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float2 t = both(0.f);
@@ -197,9 +210,9 @@ __device__ __forceinline__ void row_stats(const Eight (&v)[K][L::NV], int kind, 
       for (int q = 0; q < 4; ++q) t = add(t, v[k][i].p[q]);
     s[k] = sum_of(t);
   }
-  const float own = n > 0.f ? warp_sum_spread<K>(s) / n : 0.f;      // of the row this lane stands for
+  float mu = warp_sum_spread<K>(s) * inv_count_of<L>(sh, warp);      // of the row this lane stands for
   float m[K];
-  spread_get<K>(m, own);
+  spread_get<K>(m, mu);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float2 t = both(0.f);
@@ -213,24 +226,24 @@ __device__ __forceinline__ void row_stats(const Eight (&v)[K][L::NV], int kind, 
     s[k] = sum_of(t);
   }
   float q = warp_sum_spread<K>(s);
-  float mu = own;
   if (nwarps > 1) {
     float2* b = sh.sums.v[half] + (lane / M) * 33;
-    if (sub == 0) b[warp] = make_float2(own, q);
+    if (sub == 0) b[warp] = make_float2(mu, q);
     __syncthreads();
     float2 p[W];
-    float cw[W], total = 0.f;
+    float total = 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const int w = sub + j * M;
-      p[j] = w < nwarps ? b[w] : make_float2(0.f, 0.f);
-      cw[j] = w < nwarps ? sh.count[w] : 0.f;
-      total += cw[j] * p[j].x;
+      p[j] = b[sub + j * M];                     // warps that are not there: zeros, or (block sums) leftovers
+      total += sub + j * M < nwarps ? count_of<L>(sh, sub + j * M) * p[j].x : 0.f;
     }
     mu = spread_sum<K>(total) * inv_dim;
     q = 0.f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) q += p[j].y + cw[j] * (p[j].x - mu) * (p[j].x - mu);
+    for (int j = 0; j < W; ++j) {
+      const float off = p[j].x - mu;
+      q += sub + j * M < nwarps ? count_of<L>(sh, sub + j * M) * off * off + p[j].y : 0.f;
+    }
     q = spread_sum<K>(q);
     half ^= 1;
   }
@@ -243,10 +256,9 @@ __device__ __forceinline__ void row_stats(const Eight (&v)[K][L::NV], int kind, 
 // with u are taken about the warps' means as well and merged alike.
 template <class L, int K, int S>
 __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][L::NV], const Eight (&u)[K][L::NV], int kind, float eps,
-                                              int dim, Shared<S>& sh, int& half, int nwarps, float (&mean)[K],
-                                              float (&rstd)[K], float (&mu0)[K], float (&mu1)[K]) {
+                                              float inv_dim, int dim, Shared<S>& sh, int& half, int nwarps,
+                                              float (&mean)[K], float (&rstd)[K], float (&mu0)[K], float (&mu1)[K]) {
   constexpr int NV = L::NV;
-  const float inv_dim = 1.f / (float)dim;
   float s[2 * K];
   if (kind == kRms) {
 #pragma unroll
@@ -272,10 +284,10 @@ __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][L::NV], const 
     return;
   }
   // values of a warp: first the sums of x' and u, then the second moment and
-  // the sum of u (x' - its mean)
+  // the sum of u (x' - its mean); lanes below 16 stand for x', the others for u
   constexpr int N = 2 * K, M = 32 / N, W = (32 + M - 1) / M;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % M;
-  const float inv_n = sh.count[warp] > 0.f ? 1.f / sh.count[warp] : 0.f;
+  const bool is_x = lane < 16;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float2 t0 = both(0.f), t1 = both(0.f);
@@ -290,9 +302,10 @@ __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][L::NV], const 
     s[K + k] = sum_of(t1);
   }
   float first = warp_sum_spread<N>(s);
-  if (lane < 16) first *= inv_n;                 // lanes below 16 stand for x', the others for u
-  float m[N];
-  spread_get<N>(m, first);
+  first *= is_x ? inv_count_of<L>(sh, warp) : 1.f;
+  float m[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) m[k] = __shfl_sync(0xffffffffu, first, k * M);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float2 t0 = both(0.f), t1 = both(0.f);
@@ -308,37 +321,32 @@ __device__ __forceinline__ void row_stats_bwd(const Eight (&v)[K][L::NV], const 
     s[K + k] = sum_of(t1);
   }
   float second = warp_sum_spread<N>(s);
-  float mu = first;
   if (nwarps > 1) {
     float2* b = sh.sums.v[half] + (lane / M) * 33;
     if (sub == 0) b[warp] = make_float2(first, second);
     __syncthreads();
     const float2* bx = sh.sums.v[half] + ((lane & 15) / M) * 33;     // x' of the row this lane stands for
     float2 p[W];
-    float xm[W], cw[W], total = 0.f;
+    float total = 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const int w = sub + j * M;
-      p[j] = w < nwarps ? b[w] : make_float2(0.f, 0.f);
-      xm[j] = w < nwarps ? bx[w].x : 0.f;
-      cw[j] = w < nwarps ? sh.count[w] : 0.f;
-      total += (lane < 16 ? cw[j] : 1.f) * p[j].x;
+      p[j] = b[sub + j * M];
+      total += sub + j * M < nwarps ? (is_x ? count_of<L>(sh, sub + j * M) : 1.f) * p[j].x : 0.f;
     }
-    mu = spread_sum<N>(total);
-    if (lane < 16) mu *= inv_dim;
-    const float mx = __shfl_sync(0xffffffffu, mu, lane & 15);
+    first = spread_sum<N>(total) * (is_x ? inv_dim : 1.f);
+    const float mx = __shfl_sync(0xffffffffu, first, lane & 15);
     second = 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const float off = xm[j] - mx;
-      second += p[j].y + off * (lane < 16 ? cw[j] * off : p[j].x);
+      const float off = bx[sub + j * M].x - mx;
+      second += sub + j * M < nwarps ? off * (is_x ? count_of<L>(sh, sub + j * M) * off : p[j].x) + p[j].y : 0.f;
     }
     second = spread_sum<N>(second);
     half ^= 1;
   }
-  if (lane < 16) second = rsqrtf(second * inv_dim + eps);
+  if (is_x) second = rsqrtf(second * inv_dim + eps);
   float a[N], b2[N];
-  spread_get<N>(a, mu);
+  spread_get<N>(a, first);
   spread_get<N>(b2, second);
 #pragma unroll
   for (int k = 0; k < K; ++k) {

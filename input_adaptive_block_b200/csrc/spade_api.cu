@@ -577,6 +577,7 @@ spade_status plan_row(const spade_row_desc* D, const spade_row_params* P, bool b
   a.eps = d.eps;
   a.post_eps = d.post_eps;
   a.residual_scale = d.residual_scale;
+  a.inv_dim = 1.f / (float)d.dim;
   a.x_bf16 = d.x_dt == SPADE_BF16;
   a.branch_bf16 = d.branch_dt == SPADE_BF16;
   a.param_bf16 = d.param_dt == SPADE_BF16;

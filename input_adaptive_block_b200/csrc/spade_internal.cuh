@@ -110,7 +110,7 @@ cudaError_t launch_sics(const void* q, const void* k, const Geo* cand, int n_can
 struct RowArgs {
   long long rows, groups, rows_per_group, chunks;
   int dim, norm, post_norm;
-  float eps, post_eps, residual_scale;
+  float eps, post_eps, residual_scale, inv_dim;
   bool x_bf16, branch_bf16, param_bf16;
   const void *x, *y;                                  // forward inputs (x also backward)
   void *x_out, *h;                                    // forward outputs
