@@ -32,25 +32,35 @@ using namespace rowio;
 
 constexpr int kDepthMax = 14;
 
+// FULL: heads of 16 * lanes channels, and a unit for every thread and place.
+template <int P_, bool HALF_, bool FULL_, bool RING_, int UPT_>
+struct Layout {
+  static constexpr int P = P_, UPT = UPT_;
+  static constexpr bool HALF = HALF_, FULL = FULL_, RING = RING_;
+};
+
 // Channel of a thread's element e (0..15).  Interleaved: pairs (2m, 2m + 1)
 // are neighbours in a piece (P = 1: two single accesses).  Halves: elements
 // m and m + 8 are half a head apart.
-template <int P, bool HALF>
+template <class L>
 __device__ __forceinline__ int channel(int j, int lanes, int e, int d) {
-  constexpr int O = !HALF && P == 1 ? 2 : P;
+  constexpr int O = !L::HALF && L::P == 1 ? 2 : L::P;
+  constexpr bool HALF = L::HALF;
   if (HALF) return ((e & 7) / O * lanes + j) * O + (e & 7) % O + (e >= 8 ? d >> 1 : 0);
   return (e / O * lanes + j) * O + e % O;
 }
-template <int P, bool HALF>
+template <class L>
 __device__ __forceinline__ bool owned(int j, int lanes, int e, int d) {
-  return HALF ? channel<P, HALF>(j, lanes, e & 7, d) < (d >> 1) : channel<P, HALF>(j, lanes, e, d) < d;
+  if (L::FULL) return true;
+  return L::HALF ? channel<L>(j, lanes, e & 7, d) < (d >> 1) : channel<L>(j, lanes, e, d) < d;
 }
 // Where the cosine of pair p lies, its sine two floats on: as entry m of lane
 // j, two entries to a 16-byte word (cos, cos, sin, sin), so that a thread reads
 // its eight as four words, without bank conflicts, ready for paired arithmetic.
-template <int P, bool HALF>
+template <class L>
 __device__ __forceinline__ int angle_slot(int p, int lanes) {
-  constexpr int O = !HALF && P == 1 ? 2 : P;
+  constexpr int O = !L::HALF && L::P == 1 ? 2 : L::P;
+  constexpr bool HALF = L::HALF;
   const int c = HALF ? p : 2 * p, piece = c / O;
   const int e = piece / lanes * O + c % O, j = piece & (lanes - 1), m = HALF ? e : e >> 1;
   return ((m >> 1) * lanes + j) * 4 + (m & 1);
@@ -61,16 +71,18 @@ __device__ __forceinline__ int angle_slot(int p, int lanes) {
 struct Unit {
   float2 a[4], b[4];
 };
-template <bool HALF>
+template <class L>
 __device__ __forceinline__ void pairs_of(Unit& u, const float (&v)[16]) {
+  constexpr bool HALF = L::HALF;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     u.a[q] = HALF ? make_float2(v[2 * q], v[2 * q + 1]) : make_float2(v[4 * q], v[4 * q + 2]);
     u.b[q] = HALF ? make_float2(v[2 * q + 8], v[2 * q + 9]) : make_float2(v[4 * q + 1], v[4 * q + 3]);
   }
 }
-template <bool HALF>
+template <class L>
 __device__ __forceinline__ void elements_of(float (&v)[16], const Unit& u) {
+  constexpr bool HALF = L::HALF;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     v[HALF ? 2 * q : 4 * q] = u.a[q].x;
@@ -79,51 +91,56 @@ __device__ __forceinline__ void elements_of(float (&v)[16], const Unit& u) {
     v[HALF ? 2 * q + 9 : 4 * q + 3] = u.b[q].y;
   }
 }
-template <typename T, int P, bool HALF>
+template <typename T, class L>
 __device__ __forceinline__ void load16(Unit& u, const T* head, bool in, int j, int lanes, int d) {
+  constexpr int P = L::P;
   float v[16];
 #pragma unroll
   for (int e = 0; e < 16; e += P) {
-    if (in && owned<P, HALF>(j, lanes, e, d)) {
-      load_piece<T, P>(v + e, head + channel<P, HALF>(j, lanes, e, d));
+    if (in && owned<L>(j, lanes, e, d)) {
+      load_piece<T, P>(v + e, head + channel<L>(j, lanes, e, d));
     } else {
 #pragma unroll
       for (int q = 0; q < P; ++q) v[e + q] = 0.f;
     }
   }
-  pairs_of<HALF>(u, v);
+  pairs_of<L>(u, v);
 }
-template <typename T, int P, bool HALF>
+template <typename T, class L>
 __device__ __forceinline__ void store16(T* head, const Unit& u, int j, int lanes, int d) {
+  constexpr int P = L::P;
   float v[16];
-  elements_of<HALF>(v, u);
+  elements_of<L>(v, u);
 #pragma unroll
   for (int e = 0; e < 16; e += P)
-    if (owned<P, HALF>(j, lanes, e, d)) store_piece<P>(head + channel<P, HALF>(j, lanes, e, d), v + e);
+    if (owned<L>(j, lanes, e, d)) store_piece<P>(head + channel<L>(j, lanes, e, d), v + e);
 }
 // The ring keeps a unit's pieces [16 / P][threads][P].
-template <typename T, int P, bool HALF>
+template <typename T, class L>
 __device__ __forceinline__ void fetch16(uint32_t to, const T* head, int j, int lanes, int d) {
+  constexpr int P = L::P;
 #pragma unroll
   for (int e = 0; e < 16; e += P)
-    if (owned<P, HALF>(j, lanes, e, d))
+    if (owned<L>(j, lanes, e, d))
       copy_async<P * (int)sizeof(T)>(to + (e / P * blockDim.x + threadIdx.x) * P * (int)sizeof(T),
-                                     head + channel<P, HALF>(j, lanes, e, d));
+                                     head + channel<L>(j, lanes, e, d));
 }
-template <typename T, int P, bool HALF>
+template <typename T, class L>
 __device__ __forceinline__ void ring16(Unit& u, const unsigned char* at) {
+  constexpr int P = L::P;
   const T* p = reinterpret_cast<const T*>(at);
   float v[16];
 #pragma unroll
   for (int e = 0; e < 16; e += P) load_piece<T, P>(v + e, p + (e / P * blockDim.x + threadIdx.x) * P);
-  pairs_of<HALF>(u, v);
+  pairs_of<L>(u, v);
 }
 // What is not copied reads as zero.
-template <typename T, int P, bool HALF>
+template <typename T, class L>
 __device__ __forceinline__ void clear16(unsigned char* at, bool in, int j, int lanes, int d) {
+  constexpr int P = L::P;
 #pragma unroll
   for (int e = 0; e < 16; ++e)
-    if (!in || !owned<P, HALF>(j, lanes, e, d))
+    if (!in || !owned<L>(j, lanes, e, d))
       reinterpret_cast<T*>(at)[(e / P * blockDim.x + threadIdx.x) * P + e % P] = T(0.f);
 }
 
@@ -138,7 +155,7 @@ __device__ __forceinline__ unsigned divide(unsigned n, const QkArgs::Divisor& by
 }
 
 // Cosine and sine of every pair of the block's next tokens.
-template <int P, bool HALF, int K>
+template <class L, int K>
 __device__ __forceinline__ void angles(const QkArgs& a, const Turns& tu, long long r0, long long r1, float* cs) {
   const int half_d = a.d >> 1;
   for (int i = threadIdx.x; i < K * half_d; i += blockDim.x) {
@@ -157,7 +174,7 @@ __device__ __forceinline__ void angles(const QkArgs& a, const Turns& tu, long lo
       const double t = (double)pos * tu.turn[p];
       sincospif(2.f * (float)(t - rint(t)), &s, &c);
     }
-    float* o = cs + k * 16 * a.lanes + angle_slot<P, HALF>(p, a.lanes);
+    float* o = cs + k * 16 * a.lanes + angle_slot<L>(p, a.lanes);
     o[0] = c;
     o[2] = s;
   }
@@ -184,10 +201,12 @@ __device__ __forceinline__ void turn(Unit& u, const Angles& t, bool back) {
 }
 
 // What forward and backward share: the units of this thread and its ring.
-template <typename T, int P, bool HALF, bool RING, int UPT>
+template <typename T, class L>
 struct Units {
+  static constexpr int UPT = L::UPT;
   int j, lanes, d;
   int head[UPT];
+  float inv[UPT];                // 1 / the values that a norm of the unit runs over
   bool k_side[UPT], in[UPT];
   uint32_t slot;
 
@@ -200,7 +219,8 @@ struct Units {
       const int h = ((int)threadIdx.x + i * (int)blockDim.x) / lanes;
       k_side[i] = h >= a.heads[0];
       head[i] = h - (k_side[i] ? a.heads[0] : 0);
-      in[i] = h < a.heads[0] + a.heads[1];
+      inv[i] = a.inv_count[k_side[i]];
+      in[i] = L::FULL || h < a.heads[0] + a.heads[1];
     }
     slot = (uint32_t)(ops * UPT * 16 * sizeof(T)) * blockDim.x;
   }
@@ -219,7 +239,7 @@ struct Units {
     for (int s = 0; s < depth; ++s)
       for (int o = 0; o < ops; ++o)
 #pragma unroll
-        for (int i = 0; i < UPT; ++i) clear16<T, P, HALF>(ring + s * slot + place(o, i), in[i], j, lanes, d);
+        for (int i = 0; i < UPT; ++i) clear16<T, L>(ring + s * slot + place(o, i), in[i], j, lanes, d);
   }
   __device__ __forceinline__ void weights(Unit& w, const QkArgs& a, int i) const {
     const void* p = a.weight[k_side[i]];
@@ -228,9 +248,9 @@ struct Units {
 #pragma unroll
       for (int q = 0; q < 4; ++q) w.a[q] = w.b[q] = both(1.f);
     } else if (a.weight_bf16) {
-      load16<bf16, P, HALF>(w, static_cast<const bf16*>(p) + off, true, j, lanes, d);
+      load16<bf16, L>(w, static_cast<const bf16*>(p) + off, true, j, lanes, d);
     } else {
-      load16<float, P, HALF>(w, static_cast<const float*>(p) + off, true, j, lanes, d);
+      load16<float, L>(w, static_cast<const float*>(p) + off, true, j, lanes, d);
     }
   }
 };
@@ -249,13 +269,15 @@ __device__ __forceinline__ void read_turns(Turns& tu, const QkArgs& a, float* cs
 }
 
 // ---------------------------------------------------------------- forward --
-template <typename T, int P, bool HALF, bool RING, int UPT, int K>
-__global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const __grid_constant__ QkArgs a, int depth) {
+template <typename T, class L, int K>
+__global__ void __launch_bounds__(L::UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const __grid_constant__ QkArgs a, int depth) {
+  constexpr int UPT = L::UPT;
+  constexpr bool RING = L::RING;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Turns tu;
   __shared__ Scratch<K> sums;
   __shared__ __align__(16) float cs[2][K * 2 * SPADE_ROPE_MAX_PAIRS];
-  const Units<T, P, HALF, RING, UPT> un(a, 1);
+  const Units<T, L> un(a, 1);
   const int lanes = un.lanes, j = un.j, d = un.d, nwarps = blockDim.x >> 5;
   const long long r0 = a.rows * blockIdx.x / gridDim.x, r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
   const T* const xs[2] = {static_cast<const T*>(a.x[0]), static_cast<const T*>(a.x[1])};
@@ -276,7 +298,7 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
       for (int i = 0; i < UPT; ++i)
         if constexpr (RING)
           if (un.in[i]) {
-            fetch16<T, P, HALF>(ring_at + fs * un.slot + un.place(0, i), from[i], j, lanes, d);
+            fetch16<T, L>(ring_at + fs * un.slot + un.place(0, i), from[i], j, lanes, d);
             from[i] += un.step(a.x_stride, i);
           }
     }
@@ -295,14 +317,18 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
     for (int i = 0; i < UPT; ++i) un.weights(w[i], a, i);
   }
   read_turns(tu, a, cs[0], 4 * K * SPADE_ROPE_MAX_PAIRS);
-  angles<P, HALF, K>(a, tu, r0, r1, cs[0]);
+  angles<L, K>(a, tu, r0, r1, cs[0]);
   int half = 0, buf = 0;
   auto get = [&](Unit& v, const unsigned char* at, long long r, int i) {
-    if constexpr (RING) ring16<T, P, HALF>(v, at + un.place(0, i));
-    else load16<T, P, HALF>(v, un.at(xs, a.x_stride, r, i), un.in[i], j, lanes, d);
+    if constexpr (RING) ring16<T, L>(v, at + un.place(0, i));
+    else load16<T, L>(v, un.at(xs, a.x_stride, r, i), un.in[i], j, lanes, d);
   };
   for (long long r = r0; r < r1; r += K) {
     const int n = r1 - r < K ? (int)(r1 - r) : K;
+    // UPT, unknown to the compiler: a branch on it, never taken, keeps a later
+    // unit's loads, and so their registers, behind the unit before
+    int opaque = UPT;
+    asm volatile("" : "+r"(opaque));
     if (RING) wait_async_upto(depth - K);
     const unsigned char* at[K];
 #pragma unroll
@@ -339,8 +365,8 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        if (token) rs[k][i] = rsqrtf((un.k_side[i] ? s[K + k] : s[k]) / (float)(a.heads[un.k_side[i]] * d) + a.eps);
-        else if (normed) rs[k][i] = rsqrtf(lanes_sum(rs[k][i], lanes) / (float)d + a.eps);
+        if (token) rs[k][i] = rsqrtf((un.k_side[i] ? s[K + k] : s[k]) * un.inv[i] + a.eps);
+        else if (normed) rs[k][i] = rsqrtf(lanes_sum(rs[k][i], lanes) * un.inv[i] + a.eps);
       }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -349,6 +375,7 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
       get_angles(t, cs[buf] + k * 16 * lanes, j, lanes);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
+        if (i >= opaque) break;
         if (!un.in[i]) continue;
         Unit v;
         get(v, at[k], r + k, i);
@@ -361,7 +388,7 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
           }
         }
         turn(v, t, false);
-        store16<T, P, HALF>(to[i], v, j, lanes, d);
+        store16<T, L>(to[i], v, j, lanes, d);
         to[i] += un.step(a.out_stride, i);
       }
     }
@@ -370,35 +397,29 @@ __global__ void __launch_bounds__(UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const 
       us = us + n >= depth ? us + n - depth : us + n;
     }
     buf ^= 1;
-    if (r + K < r1) angles<P, HALF, K>(a, tu, r + K, r1, cs[buf]);    // last read before this token's barrier
+    if (r + K < r1) angles<L, K>(a, tu, r + K, r1, cs[buf]);    // last read before this token's barrier
   }
   if (RING) wait_async<0>();
 }
 
 // --------------------------------------------------------------- backward --
-template <typename T, int P, bool HALF, bool RING, int UPT, int K>
-__global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const __grid_constant__ QkArgs a, int depth) {
+template <typename T, class L, int K>
+__global__ void __launch_bounds__(L::UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const __grid_constant__ QkArgs a, int depth) {
+  constexpr int UPT = L::UPT;
+  constexpr bool RING = L::RING;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Turns tu;
   __shared__ Scratch<2 * K> sums;
   __shared__ __align__(16) float cs[2][K * 2 * SPADE_ROPE_MAX_PAIRS];
   const bool normed = a.norm != SPADE_QK_NORM_NONE, token = a.norm == SPADE_QK_NORM_TOKEN;
   const int ops = normed ? 2 : 1;
-  const Units<T, P, HALF, RING, UPT> un(a, ops);
+  const Units<T, L> un(a, ops);
   const int lanes = un.lanes, j = un.j, d = un.d, nwarps = blockDim.x >> 5;
   const long long r0 = a.rows * blockIdx.x / gridDim.x, r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
   const T* const gs[2] = {static_cast<const T*>(a.dout[0]), static_cast<const T*>(a.dout[1])};
   const T* const xs[2] = {static_cast<const T*>(a.x[0]), static_cast<const T*>(a.x[1])};
   T* const outs[2] = {static_cast<T*>(a.out[0]), static_cast<T*>(a.out[1])};
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-  const T *from_g[UPT], *from_x[UPT];     // the next token to copy and the next to write
-  T* to[UPT];
-#pragma unroll
-  for (int i = 0; i < UPT; ++i) {
-    from_g[i] = un.at(gs, a.dout_stride, r0, i);
-    from_x[i] = un.at(xs, a.x_stride, r0, i);
-    to[i] = un.at(outs, a.out_stride, r0, i);
-  }
   long long fr = r0;
   int fs = 0, us = 0;
   auto fetch = [&]() {
@@ -408,12 +429,8 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
         if constexpr (RING)
           if (un.in[i]) {
             const uint32_t slot = ring_at + fs * un.slot;
-            fetch16<T, P, HALF>(slot + un.place(0, i), from_g[i], j, lanes, d);
-            from_g[i] += un.step(a.dout_stride, i);
-            if (normed) {
-              fetch16<T, P, HALF>(slot + un.place(1, i), from_x[i], j, lanes, d);
-              from_x[i] += un.step(a.x_stride, i);
-            }
+            fetch16<T, L>(slot + un.place(0, i), un.at(gs, a.dout_stride, fr, i), j, lanes, d);
+            if (normed) fetch16<T, L>(slot + un.place(1, i), un.at(xs, a.x_stride, fr, i), j, lanes, d);
           }
     }
     commit_async();
@@ -432,16 +449,16 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
     for (int p = 0; p < 4; ++p) dw[i].a[p] = dw[i].b[p] = both(0.f);
   }
   read_turns(tu, a, cs[0], 4 * K * SPADE_ROPE_MAX_PAIRS);
-  angles<P, HALF, K>(a, tu, r0, r1, cs[0]);
+  angles<L, K>(a, tu, r0, r1, cs[0]);
   int half = 0, buf = 0;
   auto get_g = [&](Unit& v, const unsigned char* at, long long r, int i, const Angles& t) {
-    if constexpr (RING) ring16<T, P, HALF>(v, at + un.place(0, i));
-    else load16<T, P, HALF>(v, un.at(gs, a.dout_stride, r, i), un.in[i], j, lanes, d);
+    if constexpr (RING) ring16<T, L>(v, at + un.place(0, i));
+    else load16<T, L>(v, un.at(gs, a.dout_stride, r, i), un.in[i], j, lanes, d);
     turn(v, t, true);
   };
   auto get_x = [&](Unit& v, const unsigned char* at, long long r, int i) {
-    if constexpr (RING) ring16<T, P, HALF>(v, at + un.place(1, i));
-    else load16<T, P, HALF>(v, un.at(xs, a.x_stride, r, i), un.in[i], j, lanes, d);
+    if constexpr (RING) ring16<T, L>(v, at + un.place(1, i));
+    else load16<T, L>(v, un.at(xs, a.x_stride, r, i), un.in[i], j, lanes, d);
   };
   for (long long r = r0; r < r1; r += K) {
     const int n = r1 - r < K ? (int)(r1 - r) : K;
@@ -494,12 +511,11 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
           const bool ks = un.k_side[i];
           const float q0 = token ? (ks ? s[K + k] : s[k]) : lanes_sum(rs[k][i], lanes);
           const float q1 = token ? (ks ? s[3 * K + k] : s[2 * K + k]) : lanes_sum(cf[k][i], lanes);
-          const float inv = 1.f / (float)(token ? a.heads[ks] * d : d);
-          rs[k][i] = rsqrtf(q0 * inv + a.eps);
-          cf[k][i] = rs[k][i] * rs[k][i] * q1 * inv;
+          rs[k][i] = rsqrtf(q0 * un.inv[i] + a.eps);
+          cf[k][i] = rs[k][i] * rs[k][i] * q1 * un.inv[i];
         }
     }
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < K; ++k) {
       if (k >= n) break;
       Angles t;
@@ -521,8 +537,7 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
             u.b[p] = mul(f, fma(x.b[p], g, mul(u.b[p], w[i].b[p])));
           }
         }
-        store16<T, P, HALF>(to[i], u, j, lanes, d);
-        to[i] += un.step(a.out_stride, i);
+        store16<T, L>(un.at(outs, a.out_stride, r + k, i), u, j, lanes, d);
       }
     }
     if (RING) {
@@ -530,7 +545,7 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
       us = us + n >= depth ? us + n - depth : us + n;
     }
     buf ^= 1;
-    if (r + K < r1) angles<P, HALF, K>(a, tu, r + K, r1, cs[buf]);    // last read before this token's barrier
+    if (r + K < r1) angles<L, K>(a, tu, r + K, r1, cs[buf]);    // last read before this token's barrier
   }
   if (RING) wait_async<0>();
   if (!normed || !a.part) return;
@@ -543,10 +558,10 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
       if (un.in[i]) {
         float* o = part + ((un.k_side[i] ? a.heads[0] : 0) + un.head[i]) * d;
         float v[16];
-        elements_of<HALF>(v, dw[i]);
+        elements_of<L>(v, dw[i]);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (owned<P, HALF>(j, lanes, e, d)) o[channel<P, HALF>(j, lanes, e, d)] = v[e];
+          if (owned<L>(j, lanes, e, d)) o[channel<L>(j, lanes, e, d)] = v[e];
       }
     return;
   }
@@ -559,7 +574,7 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
       float v[16];
-      elements_of<HALF>(v, dw[i]);
+      elements_of<L>(v, dw[i]);
 #pragma unroll
       for (int e = 0; e < 16; ++e) sum[e] += un.k_side[i] == (t == 1) ? v[e] : 0.f;
     }
@@ -568,8 +583,8 @@ __global__ void __launch_bounds__(UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const 
       float v = sum[e];
       // the heads of one warp, then the warps through shared memory
       for (int o = lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if ((int)(threadIdx.x & 31) < lanes && owned<P, HALF>(j, lanes, e, d))
-        by_warp[(threadIdx.x >> 5) * d + channel<P, HALF>(j, lanes, e, d)] = v;
+      if ((int)(threadIdx.x & 31) < lanes && owned<L>(j, lanes, e, d))
+        by_warp[(threadIdx.x >> 5) * d + channel<L>(j, lanes, e, d)] = v;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < d; i += blockDim.x) {
@@ -644,26 +659,26 @@ cudaError_t launch(K kernel, const QkArgs& a, int grid, int threads, int blocks,
   return cudaGetLastError();
 }
 
-template <typename T, int P, bool HALF, bool RING, int UPT>
+template <typename T, class L>
 cudaError_t run_fwd(const QkArgs& a, cudaStream_t s) {
   constexpr int K = 2;
   const int threads = block_threads(a);
-  const size_t slot = (size_t)threads * UPT * 16 * sizeof(T);
-  const int blocks = blocks_of(threads, 640, RING ? slot : 0, K);
-  return launch(qk_fwd_kernel<T, P, HALF, RING, UPT, K>, a, grid_of(a, blocks, K), threads, blocks, K, slot, RING, 0, s);
+  const size_t slot = (size_t)threads * L::UPT * 16 * sizeof(T);
+  const int blocks = blocks_of(threads, 640, L::RING ? slot : 0, K);
+  return launch(qk_fwd_kernel<T, L, K>, a, grid_of(a, blocks, K), threads, blocks, K, slot, L::RING, 0, s);
 }
 
 // Blocks of an SM of the backward pass at most (bfloat16 rows).
 int bwd_blocks(const QkArgs& a) { return blocks_of(block_threads(a), 512, 0, 0); }
 
-template <typename T, int P, bool HALF, bool RING, int UPT>
+template <typename T, class L>
 cudaError_t run_bwd(const QkArgs& a, cudaStream_t s) {
   constexpr int K = sizeof(T) == 2 ? 2 : 1;
   const int threads = block_threads(a);
-  const size_t slot = (size_t)threads * UPT * 16 * sizeof(T) * (a.norm != SPADE_QK_NORM_NONE ? 2 : 1);
+  const size_t slot = (size_t)threads * L::UPT * 16 * sizeof(T) * (a.norm != SPADE_QK_NORM_NONE ? 2 : 1);
   const size_t least = a.norm == SPADE_QK_NORM_HEAD ? (size_t)(threads / 32) * a.d * sizeof(float) : 0;
-  const int blocks = blocks_of(threads, 512, RING ? slot : 0, K == 1 ? 3 : K), grid = grid_of(a, blocks, K);
-  cudaError_t e = launch(qk_bwd_kernel<T, P, HALF, RING, UPT, K>, a, grid, threads, blocks, K, slot, RING, least, s);
+  const int blocks = blocks_of(threads, 512, L::RING ? slot : 0, K == 1 ? 3 : K), grid = grid_of(a, blocks, K);
+  cudaError_t e = launch(qk_bwd_kernel<T, L, K>, a, grid, threads, blocks, K, slot, L::RING, least, s);
   if (e != cudaSuccess || !a.part) return e;
   const bool token = a.norm == SPADE_QK_NORM_TOKEN;
   const int wq = token ? a.heads[0] * a.d : a.d, wk = token ? a.heads[1] * a.d : a.d;
@@ -673,15 +688,24 @@ cudaError_t run_bwd(const QkArgs& a, cudaStream_t s) {
 
 // Threads of four units read tokens where they are used: two tokens of so
 // many channels need not fit in shared memory.
-template <typename T, int P, bool RING>
+template <typename T, int P, bool HALF, bool RING, bool WIDE>
 cudaError_t by_shape(const QkArgs& a, bool back, cudaStream_t s) {
-  const bool two = units_per_thread(a) == 2;
-  if (back) {
-    if (a.half) return two ? run_bwd<T, P, true, RING, 2>(a, s) : run_bwd<T, P, true, false, 4>(a, s);
-    return two ? run_bwd<T, P, false, RING, 2>(a, s) : run_bwd<T, P, false, false, 4>(a, s);
+  if (units_per_thread(a) == 4) {
+    using L = Layout<P, HALF, false, false, 4>;
+    return back ? run_bwd<T, L>(a, s) : run_fwd<T, L>(a, s);
   }
-  if (a.half) return two ? run_fwd<T, P, true, RING, 2>(a, s) : run_fwd<T, P, true, false, 4>(a, s);
-  return two ? run_fwd<T, P, false, RING, 2>(a, s) : run_fwd<T, P, false, false, 4>(a, s);
+  if constexpr (WIDE) {
+    if (a.d == 16 * a.lanes && (a.heads[0] + a.heads[1]) * a.lanes == 2 * block_threads(a)) {
+      using L = Layout<P, HALF, true, RING, 2>;
+      return back ? run_bwd<T, L>(a, s) : run_fwd<T, L>(a, s);
+    }
+  }
+  using L = Layout<P, HALF, false, RING, 2>;
+  return back ? run_bwd<T, L>(a, s) : run_fwd<T, L>(a, s);
+}
+template <typename T, int P, bool RING, bool WIDE>
+cudaError_t by_style(const QkArgs& a, bool back, cudaStream_t s) {
+  return a.half ? by_shape<T, P, true, RING, WIDE>(a, back, s) : by_shape<T, P, false, RING, WIDE>(a, back, s);
 }
 
 // The widest piece, in channels, that heads (halves of heads) and every row
@@ -706,10 +730,10 @@ int piece_of(const QkArgs& a, int size) {
 cudaError_t run(const QkArgs& a, bool is_bf16, bool back, cudaStream_t s) {
   const int p = piece_of(a, is_bf16 ? 2 : 4);
   if (is_bf16) {
-    if (p == 8) return by_shape<bf16, 8, true>(a, back, s);
-    return p == 2 ? by_shape<bf16, 2, true>(a, back, s) : by_shape<bf16, 1, false>(a, back, s);
+    if (p == 8) return by_style<bf16, 8, true, true>(a, back, s);
+    return p == 2 ? by_style<bf16, 2, true, false>(a, back, s) : by_style<bf16, 1, false, false>(a, back, s);
   }
-  return p == 4 ? by_shape<float, 4, true>(a, back, s) : by_shape<float, 1, true>(a, back, s);
+  return p == 4 ? by_style<float, 4, true, true>(a, back, s) : by_style<float, 1, true, false>(a, back, s);
 }
 
 }  // namespace

@@ -186,7 +186,8 @@ __device__ __forceinline__ void block_sum(float (&v)[N], Scratch<M>& sh, int& ha
     if (sub == 0) b[threadIdx.x >> 5] = s;
     __syncthreads();
     s = 0.f;
-    for (int w = sub; w < nwarps; w += L) s += b[w];
+#pragma unroll
+    for (int w = 0; w < 32; w += L) s += w + sub < nwarps ? b[w + sub] : 0.f;
     s = spread_sum<N>(s);
     half ^= 1;
   }

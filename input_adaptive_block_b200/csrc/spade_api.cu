@@ -445,6 +445,8 @@ spade_status plan_qk(const spade_qk_desc* D, const spade_rope* rope, const int32
   a.eps = d.eps;
   a.weight_bf16 = d.weight_dt == SPADE_BF16;
   for (a.lanes = 1; a.lanes * 16 < d.d;) a.lanes *= 2;
+  for (int t = 0; t < 2; ++t)
+    a.inv_count[t] = 1.f / (float)(d.norm == SPADE_QK_NORM_TOKEN ? std::max(a.heads[t], 1) * d.d : d.d);
   spade_status st;
   const int64_t strides[6] = {d.q_stride, d.k_stride, d.q_out_stride, d.k_out_stride, d.q_dout_stride, d.k_dout_stride};
   long long* to[6] = {&a.x_stride[0], &a.x_stride[1], &a.out_stride[0], &a.out_stride[1], &a.dout_stride[0],
@@ -503,10 +505,6 @@ spade_status bind_qk(const spade_qk_desc* D, QkArgs& a, const void* const x[2], 
   const int es = dtype_size(D->dt), ws = dtype_size(D->weight_dt);
   Regions rs;
   spade_status st;
-  a.vec = a.d % 16 == 0;
-  auto vec16 = [&](const void* p, long long stride_bytes) {
-    a.vec = a.vec && aligned16(p) && stride_bytes % 16 == 0;
-  };
   for (int t = 0; t < 2; ++t) {
     if (!a.heads[t]) {
       if (dw && dw[t]) return fail(SPADE_ERR_INVALID, "weight gradient of an absent tensor");
@@ -526,10 +524,6 @@ spade_status bind_qk(const spade_qk_desc* D, QkArgs& a, const void* const x[2], 
     a.out[t] = out[t];
     a.weight[t] = w[t];
     a.dweight[t] = dw ? dw[t] : nullptr;
-    if (a.x[t]) vec16(a.x[t], a.x_stride[t] * es);
-    if (a.dout[t]) vec16(a.dout[t], a.dout_stride[t] * es);
-    vec16(a.out[t], a.out_stride[t] * es);
-    if (w[t]) vec16(w[t], 0);
     rs.add(xn[t], a.x[t], a.rows, a.x_stride[t] * es, len * es, false, true);
     rs.add(gn[t], a.dout[t], a.rows, a.dout_stride[t] * es, len * es, false, true);
     rs.add(on[t], a.out[t], a.rows, a.out_stride[t] * es, len * es, true, true);

@@ -143,7 +143,8 @@ struct QkArgs {
   int heads[2], d, lanes;          // lanes: threads per head, a power of two
   int norm;
   float eps;
-  bool weight_bf16, half, vec;
+  float inv_count[2];              // 1 / the values that a norm runs over
+  bool weight_bf16, half;
   const void* x[2];                // raw rows
   const void* dout[2];             // backward: gradient coming in
   void* out[2];                    // forward: result; backward: gradient going out
