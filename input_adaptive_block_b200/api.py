@@ -430,9 +430,20 @@ def _strided(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dt
     return t.data_ptr(), t.stride(0)
 
 
+def _output(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dtype):
+    """(tensor, pointer, row stride) of an output: a new packed one where none
+    is given."""
+    if t is None:
+        t = _new(like, shape, dtype)
+        return t, t.data_ptr(), 0
+    return (t, *_strided(t, name, like, shape, dtype))
+
+
 def _vector(t: Optional[torch.Tensor], name: str, like: torch.Tensor, n: int, dtype) -> Optional[int]:
     if t is None:
         return None
+    if t.dtype is dtype and t.is_contiguous() and t.numel() == n and t.is_cuda and t.get_device() == like.get_device():
+        return t.data_ptr()
     _on_gpu(t, name, like)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous elements")
@@ -476,12 +487,10 @@ def _qk_desc(q, k, q_weight, k_weight, grid, positions, token_offset, text_token
     if like.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != like.shape[0] or k.shape[2] != like.shape[2])):
         raise ValueError("q and k are [rows, heads, d]")
     rows, _, d = like.shape
-    desc = SpadeQkDesc()
-    desc.rows, desc.text_tokens, desc.token_offset = rows, int(text_tokens), int(token_offset)
-    desc.q_heads, desc.k_heads, desc.d = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], d
     wdt = _param_dtype((q_weight, k_weight))
-    desc.dt, desc.weight_dt = dtype_code(like.dtype), dtype_code(wdt)
-    desc.norm, desc.eps = _code(QK_NORM, norm, "norm"), eps
+    desc = SpadeQkDesc(rows, int(text_tokens), int(token_offset), 0, 0, 0, 0 if q is None else q.shape[1],
+                       0 if k is None else k.shape[1], d, dtype_code(like.dtype), dtype_code(wdt),
+                       _code(QK_NORM, norm, "norm"), eps)
     pos = None
     if positions is not None:
         if grid is not None or token_offset:
@@ -520,16 +529,13 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: Spa
     k_out)."""
     desc, like, pos, (qw, kw) = _qk_desc(q, k, q_weight, k_weight, grid, positions, token_offset, text_tokens, norm, eps)
     with _On(like, stream) as s:
-        if q is not None and q_out is None:
-            q_out = _new(q, q.shape, q.dtype)
-        if k is not None and k_out is None:
-            k_out = _new(k, k.shape, k.dtype)
-        rows, d, dt = desc.rows, desc.d, like.dtype
-        qs, ks = (rows, desc.q_heads, d), (rows, desc.k_heads, d)
-        qp, desc.q_stride = _strided(q, "q", like, qs, dt)
-        kp, desc.k_stride = _strided(k, "k", like, ks, dt)
-        qo, desc.q_out_stride = _strided(q_out if q is not None else None, "q_out", like, qs, dt)
-        ko, desc.k_out_stride = _strided(k_out if k is not None else None, "k_out", like, ks, dt)
+        dt, qo, ko = like.dtype, None, None
+        qp, desc.q_stride = _strided(q, "q", like, None if q is None else q.shape, dt)
+        kp, desc.k_stride = _strided(k, "k", like, None if k is None else k.shape, dt)
+        if q is not None:
+            q_out, qo, desc.q_out_stride = _output(q_out, "q_out", q, q.shape, dt)
+        if k is not None:
+            k_out, ko, desc.k_out_stride = _output(k_out, "k_out", k, k.shape, dt)
         check(_lib.load().spade_qk_norm_rope(ctypes.byref(desc), ctypes.byref(rope), pos, qp, kp, qw, kw, qo, ko, s),
               "spade_qk_norm_rope")
     return (q_out if q is not None else None), (k_out if k is not None else None)
@@ -557,17 +563,16 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
     with _On(like, stream) as s:
         rows, d, dt = desc.rows, desc.d, like.dtype
         qs, ks = (rows, desc.q_heads, d), (rows, desc.k_heads, d)
-        if dq_out is not None and dq is None:
-            dq = _new(dq_out, qs, dt)
-        if dk_out is not None and dk is None:
-            dk = _new(dk_out, ks, dt)
+        qo, ko = None, None
         gq, desc.q_dout_stride = _strided(dq_out, "dq_out", like, qs, dt)
         gk, desc.k_dout_stride = _strided(dk_out, "dk_out", like, ks, dt)
         normed = norm != "none"
         qp, desc.q_stride = _strided(q if normed and dq_out is not None else None, "q", like, qs, dt)
         kp, desc.k_stride = _strided(k if normed and dk_out is not None else None, "k", like, ks, dt)
-        qo, desc.q_out_stride = _strided(dq if dq_out is not None else None, "dq", like, qs, dt)
-        ko, desc.k_out_stride = _strided(dk if dk_out is not None else None, "dk", like, ks, dt)
+        if dq_out is not None:
+            dq, qo, desc.q_out_stride = _output(dq, "dq", dq_out, qs, dt)
+        if dk_out is not None:
+            dk, ko, desc.k_out_stride = _output(dk, "dk", dk_out, ks, dt)
         dqw, dkw = (None if w is None else _new(w, w.shape, torch.float32) for w in (q_weight, k_weight))
         lib = _lib.load()
         need = int(lib.spade_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(desc))) if dqw is not None or dkw is not None else 0
@@ -579,6 +584,9 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
     return QkGrads(dq if dq_out is not None else None, dk if dk_out is not None else None, dqw, dkw)
 
 
+_PER_GROUP = frozenset(("gate", "scale", "shift"))
+
+
 def _row_call(like, x_dtype, branch_dtype, norm="none", eps=0.0, post_norm="none", post_eps=0.0, residual_scale=1.0,
               gate=None, post_weight=None, weight=None, bias=None, scale=None, shift=None):
     """Descriptor and parameters of a row pass over `like` [rows, dim]."""
@@ -586,33 +594,34 @@ def _row_call(like, x_dtype, branch_dtype, norm="none", eps=0.0, post_norm="none
     if like.dim() != 2:
         raise ValueError("rows are [rows, dim]")
     rows, dim = like.shape
-    desc, params = SpadeRowDesc(), SpadeRowParams()
+    params, strides, groups = SpadeRowParams(), None, None
     given = {"gate": gate, "post_weight": post_weight, "weight": weight, "bias": bias, "scale": scale, "shift": shift}
     pdt = _param_dtype(given.values())
-    groups = None
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+    for name, t in given.items():
         if t is None:
             continue
-        if t.dim() not in (1, 2) or t.shape[-1] != dim:
-            raise ValueError(f"{name} must be [groups, {dim}] or [{dim}]")
-        g = t.shape[0] if t.dim() == 2 else 1
-        if groups is not None and groups != g:
-            raise ValueError("gate, scale and shift must have one number of groups")
-        groups = g
-        p, stride = _strided(t if t.dim() == 2 else t.unsqueeze(0), name, like, (g, dim), pdt)
+        if name in _PER_GROUP:
+            if t.dim() not in (1, 2) or t.shape[-1] != dim:
+                raise ValueError(f"{name} must be [groups, {dim}] or [{dim}]")
+            g = t.shape[0] if t.dim() == 2 else 1
+            if groups is not None and groups != g:
+                raise ValueError("gate, scale and shift must have one number of groups")
+            groups = g
+            p, stride = _strided(t if t.dim() == 2 else t.unsqueeze(0), name, like, (g, dim), pdt)
+            if stride:
+                strides = strides or {}
+                strides[name] = stride
+        else:
+            p = _vector(t, name, like, dim, pdt)
         setattr(params, name, p)
-        if stride:
-            setattr(desc, name + "_stride", stride)
     groups = 1 if groups is None else groups
     if groups < 1 or rows % groups:
         raise ValueError(f"{rows} rows in {groups} groups")
-    for name, t in (("post_weight", post_weight), ("weight", weight), ("bias", bias)):
-        if t is not None:
-            setattr(params, name, _vector(t, name, like, dim, pdt))
-    desc.rows, desc.groups, desc.dim = rows, groups, dim
-    desc.x_dt, desc.branch_dt, desc.param_dt = dtype_code(x_dtype), dtype_code(branch_dtype), dtype_code(pdt)
-    desc.norm, desc.post_norm = _code(NORM, norm, "norm"), _code(NORM, post_norm, "post_norm")
-    desc.eps, desc.post_eps, desc.residual_scale = eps, post_eps, residual_scale
+    desc = SpadeRowDesc(rows, groups, dim, dtype_code(x_dtype), dtype_code(branch_dtype), dtype_code(pdt),
+                        _code(NORM, norm, "norm"), _code(NORM, post_norm, "post_norm"), eps, post_eps, residual_scale)
+    if strides:
+        for name, stride in strides.items():
+            setattr(desc, name + "_stride", stride)
     return desc, params, given
 
 
@@ -646,10 +655,8 @@ def norm_modulate(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
     odt = out.dtype if out is not None else (out_dtype or x.dtype)
     desc, params, _ = _row_call(x, x.dtype, odt, norm, eps, weight=weight, bias=bias, scale=scale, shift=shift)
     with _On(x, stream) as s:
-        if out is None:
-            out = _new(x, x.shape, odt)
         xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
-        op, desc.h_stride = _strided(out, "out", x, x.shape, odt)
+        out, op, desc.h_stride = _output(out, "out", x, x.shape, odt)
         check(_lib.load().spade_norm_modulate(ctypes.byref(desc), ctypes.byref(params), xp, op, s), "spade_norm_modulate")
     return out
 
@@ -664,12 +671,10 @@ def norm_modulate_backward(dout: torch.Tensor, x: torch.Tensor, weight: Optional
     (dres itself is allowed)."""
     desc, params, given = _row_call(x, x.dtype, dout.dtype, norm, eps, weight=weight, bias=bias, scale=scale, shift=shift)
     with _On(x, stream) as s:
-        if dx is None:
-            dx = _new(x, x.shape, x.dtype)
         xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
         hp, desc.dh_stride = _strided(dout, "dout", x, x.shape, dout.dtype)
         rp, desc.dx_out_stride = _strided(dres, "dres", x, x.shape, x.dtype)
-        dp, desc.dx_stride = _strided(dx, "dx", x, x.shape, x.dtype)
+        dx, dp, desc.dx_stride = _output(dx, "dx", x, x.shape, x.dtype)
         out, grads = _row_grads(given, x)
         lib = _lib.load()
         wp, wn, workspace = _scratch(workspace, int(lib.spade_row_bwd_workspace_bytes(ctypes.byref(desc))), x)
@@ -687,11 +692,9 @@ def gate_residual(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor]
     desc, params, _ = _row_call(x, x.dtype, y.dtype, post_norm=post_norm, post_eps=post_eps,
                                 residual_scale=residual_scale, gate=gate, post_weight=post_weight)
     with _On(x, stream) as s:
-        if out is None:
-            out = _new(x, x.shape, x.dtype)
         xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
         yp, desc.y_stride = _strided(y, "y", x, x.shape, y.dtype)
-        op, desc.x_out_stride = _strided(out, "out", x, x.shape, x.dtype)
+        out, op, desc.x_out_stride = _output(out, "out", x, x.shape, x.dtype)
         check(_lib.load().spade_gate_residual(ctypes.byref(desc), ctypes.byref(params), xp, yp, op, s),
               "spade_gate_residual")
     return out
@@ -706,11 +709,9 @@ def gate_residual_backward(dout: torch.Tensor, y: torch.Tensor, gate: Optional[t
     desc, params, given = _row_call(dout, dout.dtype, y.dtype, post_norm=post_norm, post_eps=post_eps,
                                     residual_scale=residual_scale, gate=gate, post_weight=post_weight)
     with _On(dout, stream) as s:
-        if dy is None:
-            dy = _new(y, y.shape, y.dtype)
         gp, desc.dx_out_stride = _strided(dout, "dout", dout, dout.shape, dout.dtype)
         yp, desc.y_stride = _strided(y, "y", dout, dout.shape, y.dtype)
-        dp, desc.dy_stride = _strided(dy, "dy", dout, dout.shape, y.dtype)
+        dy, dp, desc.dy_stride = _output(dy, "dy", y, dout.shape, y.dtype)
         out, grads = _row_grads(given, dout)
         lib = _lib.load()
         wp, wn, workspace = _scratch(workspace, int(lib.spade_row_bwd_workspace_bytes(ctypes.byref(desc))), dout)
@@ -732,14 +733,10 @@ def gate_residual_norm(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Te
     desc, params, _ = _row_call(x, x.dtype, y.dtype, norm, eps, post_norm, post_eps, residual_scale, gate, post_weight,
                                 weight, bias, scale, shift)
     with _On(x, stream) as s:
-        if x_out is None:
-            x_out = _new(x, x.shape, x.dtype)
-        if out is None:
-            out = _new(y, y.shape, y.dtype)
         xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
         yp, desc.y_stride = _strided(y, "y", x, x.shape, y.dtype)
-        op, desc.x_out_stride = _strided(x_out, "x_out", x, x.shape, x.dtype)
-        hp, desc.h_stride = _strided(out, "out", x, x.shape, y.dtype)
+        x_out, op, desc.x_out_stride = _output(x_out, "x_out", x, x.shape, x.dtype)
+        out, hp, desc.h_stride = _output(out, "out", y, x.shape, y.dtype)
         check(_lib.load().spade_gate_residual_norm(ctypes.byref(desc), ctypes.byref(params), xp, yp, op, hp, s),
               "spade_gate_residual_norm")
     return x_out, out
@@ -759,16 +756,12 @@ def gate_residual_norm_backward(dx_out: Optional[torch.Tensor], dout: torch.Tens
     desc, params, given = _row_call(x, x.dtype, y.dtype, norm, eps, post_norm, post_eps, residual_scale, gate, post_weight,
                                     weight, bias, scale, shift)
     with _On(x, stream) as s:
-        if dx is None:
-            dx = _new(x, x.shape, x.dtype)
-        if dy is None:
-            dy = _new(y, y.shape, y.dtype)
         gp, desc.dx_out_stride = _strided(dx_out, "dx_out", x, x.shape, x.dtype)
         hp, desc.dh_stride = _strided(dout, "dout", x, x.shape, y.dtype)
         xp, desc.x_stride = _strided(x, "x", x, x.shape, x.dtype)
         yp, desc.y_stride = _strided(y, "y", x, x.shape, y.dtype)
-        dxp, desc.dx_stride = _strided(dx, "dx", x, x.shape, x.dtype)
-        dyp, desc.dy_stride = _strided(dy, "dy", x, x.shape, y.dtype)
+        dx, dxp, desc.dx_stride = _output(dx, "dx", x, x.shape, x.dtype)
+        dy, dyp, desc.dy_stride = _output(dy, "dy", y, x.shape, y.dtype)
         out, grads = _row_grads(given, x)
         lib = _lib.load()
         wp, wn, workspace = _scratch(workspace, int(lib.spade_row_bwd_workspace_bytes(ctypes.byref(desc))), x)

@@ -31,6 +31,7 @@ namespace {
 using namespace rowio;
 
 constexpr int kDepthMax = 14;
+constexpr int kAhead = 4;        // tokens whose angles are made at once, spread over the block
 
 // FULL: heads of 16 * lanes channels, and a unit for every thread and place.
 template <int P_, bool HALF_, bool FULL_, bool RING_, int UPT_>
@@ -154,12 +155,18 @@ __device__ __forceinline__ unsigned divide(unsigned n, const QkArgs::Divisor& by
   return (unsigned)(((unsigned long long)n * by.mul) >> by.shift);
 }
 
-// Cosine and sine of every pair of the block's next tokens.
-template <class L, int K>
+// Cosine and sine of every pair of the block's next kAhead tokens.
+template <class L>
 __device__ __forceinline__ void angles(const QkArgs& a, const Turns& tu, long long r0, long long r1, float* cs) {
   const int half_d = a.d >> 1;
-  for (int i = threadIdx.x; i < K * half_d; i += blockDim.x) {
-    const int k = K == 2 && i >= half_d ? 1 : 0, p = i - k * half_d;
+  for (int i = threadIdx.x; i < kAhead * half_d; i += blockDim.x) {
+    int k = 0, p = i;
+#pragma unroll
+    for (int m = 1; m < kAhead; ++m)
+      if (p >= half_d) {
+        p -= half_d;
+        ++k;
+      }
     const long long r = r0 + k;
     float c = 1.f, s = 0.f;
     if (p < a.pairs && r < a.video_rows && r < r1) {
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(L::UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(con
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Turns tu;
   __shared__ Scratch<K> sums;
-  __shared__ __align__(16) float cs[2][K * 2 * SPADE_ROPE_MAX_PAIRS];
+  __shared__ __align__(16) float cs[2][kAhead * 2 * SPADE_ROPE_MAX_PAIRS];
   const Units<T, L> un(a, 1);
   const int lanes = un.lanes, j = un.j, d = un.d, nwarps = blockDim.x >> 5;
   const long long r0 = a.rows * blockIdx.x / gridDim.x, r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
@@ -316,9 +323,9 @@ __global__ void __launch_bounds__(L::UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(con
 #pragma unroll
     for (int i = 0; i < UPT; ++i) un.weights(w[i], a, i);
   }
-  read_turns(tu, a, cs[0], 4 * K * SPADE_ROPE_MAX_PAIRS);
-  angles<L, K>(a, tu, r0, r1, cs[0]);
-  int half = 0, buf = 0;
+  read_turns(tu, a, cs[0], 4 * kAhead * SPADE_ROPE_MAX_PAIRS);
+  angles<L>(a, tu, r0, r1, cs[0]);
+  int half = 0, buf = 0, ago = 0;      // which angles, and how many of their tokens are done
   auto get = [&](Unit& v, const unsigned char* at, long long r, int i) {
     if constexpr (RING) ring16<T, L>(v, at + un.place(0, i));
     else load16<T, L>(v, un.at(xs, a.x_stride, r, i), un.in[i], j, lanes, d);
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(L::UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(con
     for (int k = 0; k < K; ++k) {
       if (k >= n) break;
       Angles t;
-      get_angles(t, cs[buf] + k * 16 * lanes, j, lanes);
+      get_angles(t, cs[buf] + (ago + k) * 16 * lanes, j, lanes);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         if (i >= opaque) break;
@@ -396,21 +403,26 @@ __global__ void __launch_bounds__(L::UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(con
       for (int k = 0; k < n; ++k) fetch();
       us = us + n >= depth ? us + n - depth : us + n;
     }
-    buf ^= 1;
-    if (r + K < r1) angles<L, K>(a, tu, r + K, r1, cs[buf]);    // last read before this token's barrier
+    ago += K;
+    if (ago == kAhead) {         // the next ones, where those before these were: last read before this barrier
+      ago = 0;
+      buf ^= 1;
+      if (r + K < r1) angles<L>(a, tu, r + K, r1, cs[buf]);
+    }
   }
   if (RING) wait_async<0>();
 }
 
 // --------------------------------------------------------------- backward --
 template <typename T, class L, int K>
-__global__ void __launch_bounds__(L::UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(const __grid_constant__ QkArgs a, int depth) {
+__global__ void __maxnreg__(L::UPT == 1 ? 96 : (L::UPT == 2 ? 128 : 64)) qk_bwd_kernel(const __grid_constant__ QkArgs a, int depth) {
   constexpr int UPT = L::UPT;
+  constexpr bool KEEP = UPT == 1;          // tokens stay in registers between the two passes over them
   constexpr bool RING = L::RING;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Turns tu;
   __shared__ Scratch<2 * K> sums;
-  __shared__ __align__(16) float cs[2][K * 2 * SPADE_ROPE_MAX_PAIRS];
+  __shared__ __align__(16) float cs[2][kAhead * 2 * SPADE_ROPE_MAX_PAIRS];
   const bool normed = a.norm != SPADE_QK_NORM_NONE, token = a.norm == SPADE_QK_NORM_TOKEN;
   const int ops = normed ? 2 : 1;
   const Units<T, L> un(a, ops);
@@ -420,6 +432,15 @@ __global__ void __launch_bounds__(L::UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(con
   const T* const xs[2] = {static_cast<const T*>(a.x[0]), static_cast<const T*>(a.x[1])};
   T* const outs[2] = {static_cast<T*>(a.out[0]), static_cast<T*>(a.out[1])};
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  // with one unit: the next token to copy and the next to write (with more
+  // units their registers cost more than the products they save)
+  const T *from_g = nullptr, *from_x = nullptr;
+  T* to = nullptr;
+  if constexpr (KEEP) {
+    from_g = un.at(gs, a.dout_stride, r0, 0);
+    from_x = un.at(xs, a.x_stride, r0, 0);
+    to = un.at(outs, a.out_stride, r0, 0);
+  }
   long long fr = r0;
   int fs = 0, us = 0;
   auto fetch = [&]() {
@@ -429,8 +450,17 @@ __global__ void __launch_bounds__(L::UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(con
         if constexpr (RING)
           if (un.in[i]) {
             const uint32_t slot = ring_at + fs * un.slot;
-            fetch16<T, L>(slot + un.place(0, i), un.at(gs, a.dout_stride, fr, i), j, lanes, d);
-            if (normed) fetch16<T, L>(slot + un.place(1, i), un.at(xs, a.x_stride, fr, i), j, lanes, d);
+            if constexpr (KEEP) {
+              fetch16<T, L>(slot + un.place(0, i), from_g, j, lanes, d);
+              from_g += un.step(a.dout_stride, i);
+              if (normed) {
+                fetch16<T, L>(slot + un.place(1, i), from_x, j, lanes, d);
+                from_x += un.step(a.x_stride, i);
+              }
+            } else {
+              fetch16<T, L>(slot + un.place(0, i), un.at(gs, a.dout_stride, fr, i), j, lanes, d);
+              if (normed) fetch16<T, L>(slot + un.place(1, i), un.at(xs, a.x_stride, fr, i), j, lanes, d);
+            }
           }
     }
     commit_async();
@@ -448,9 +478,9 @@ __global__ void __launch_bounds__(L::UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(con
 #pragma unroll
     for (int p = 0; p < 4; ++p) dw[i].a[p] = dw[i].b[p] = both(0.f);
   }
-  read_turns(tu, a, cs[0], 4 * K * SPADE_ROPE_MAX_PAIRS);
-  angles<L, K>(a, tu, r0, r1, cs[0]);
-  int half = 0, buf = 0;
+  read_turns(tu, a, cs[0], 4 * kAhead * SPADE_ROPE_MAX_PAIRS);
+  angles<L>(a, tu, r0, r1, cs[0]);
+  int half = 0, buf = 0, ago = 0;      // which angles, and how many of their tokens are done
   auto get_g = [&](Unit& v, const unsigned char* at, long long r, int i, const Angles& t) {
     if constexpr (RING) ring16<T, L>(v, at + un.place(0, i));
     else load16<T, L>(v, un.at(gs, a.dout_stride, r, i), un.in[i], j, lanes, d);
@@ -460,37 +490,52 @@ __global__ void __launch_bounds__(L::UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(con
     if constexpr (RING) ring16<T, L>(v, at + un.place(1, i));
     else load16<T, L>(v, un.at(xs, a.x_stride, r, i), un.in[i], j, lanes, d);
   };
+  auto next = [&](int n) {       // n tokens are used: copy as many, ahead
+    if (RING) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (k < n) fetch();
+      us = us + n >= depth ? us + n - depth : us + n;
+    }
+  };
   for (long long r = r0; r < r1; r += K) {
     const int n = r1 - r < K ? (int)(r1 - r) : K;
     if (RING) wait_async_upto(depth - K);
-    __syncthreads();                             // the angles are there
+    if (ago == 0) __syncthreads();               // the angles are there
     const unsigned char* at[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) at[k] = ring + (us + k >= depth ? us + k - depth : us + k) * un.slot;
     // per token and tensor: sum of x^2, sum of w u x; then 1 / deviation and rstd^2 mean(w u x)
     float s[4 * K], rs[K][UPT], cf[K][UPT];
-    if (normed) {
+    Unit xk[KEEP ? K : 1], uk[KEEP ? K : 1];
+    if (normed || KEEP) {
 #pragma unroll
       for (int i = 0; i < 4 * K; ++i) s[i] = 0.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         Angles t;
-        get_angles(t, cs[buf] + k * 16 * lanes, j, lanes);
+        get_angles(t, cs[buf] + (ago + k) * 16 * lanes, j, lanes);
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
           float q0 = 0.f, q1 = 0.f;
           if (k < n) {
             Unit x, u;
-            float2 s0 = both(0.f), s1 = both(0.f);
-            get_x(x, at[k], r + k, i);
             get_g(u, at[k], r + k, i, t);
+            if (normed) {
+              float2 s0 = both(0.f), s1 = both(0.f);
+              get_x(x, at[k], r + k, i);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              s0 = fma(x.b[p], x.b[p], fma(x.a[p], x.a[p], s0));
-              s1 = fma(mul(u.b[p], w[i].b[p]), x.b[p], fma(mul(u.a[p], w[i].a[p]), x.a[p], s1));
+              for (int p = 0; p < 4; ++p) {
+                s0 = fma(x.b[p], x.b[p], fma(x.a[p], x.a[p], s0));
+                s1 = fma(mul(u.b[p], w[i].b[p]), x.b[p], fma(mul(u.a[p], w[i].a[p]), x.a[p], s1));
+              }
+              q0 = sum_of(s0);
+              q1 = sum_of(s1);
             }
-            q0 = sum_of(s0);
-            q1 = sum_of(s1);
+            if constexpr (KEEP) {
+              xk[k] = x;
+              uk[k] = u;
+            }
           }
           if (un.k_side[i]) {
             s[K + k] += q0;
@@ -503,49 +548,66 @@ __global__ void __launch_bounds__(L::UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(con
           cf[k][i] = q1;
         }
       }
+      if (KEEP) next(n);
       if (token) block_sum(s, sums, half, nwarps);
+      if (normed) {
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-          const bool ks = un.k_side[i];
-          const float q0 = token ? (ks ? s[K + k] : s[k]) : lanes_sum(rs[k][i], lanes);
-          const float q1 = token ? (ks ? s[3 * K + k] : s[2 * K + k]) : lanes_sum(cf[k][i], lanes);
-          rs[k][i] = rsqrtf(q0 * un.inv[i] + a.eps);
-          cf[k][i] = rs[k][i] * rs[k][i] * q1 * un.inv[i];
-        }
-    }
-#pragma unroll 1
-    for (int k = 0; k < K; ++k) {
-      if (k >= n) break;
-      Angles t;
-      get_angles(t, cs[buf] + k * 16 * lanes, j, lanes);
-#pragma unroll
-      for (int i = 0; i < UPT; ++i) {
-        if (!un.in[i]) continue;                 // absent heads stay out of dw whatever eps makes of their zeros
-        Unit u;
-        get_g(u, at[k], r + k, i, t);
-        if (normed) {
-          Unit x;
-          get_x(x, at[k], r + k, i);
-          const float2 f = both(rs[k][i]), g = both(-cf[k][i]);
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            dw[i].a[p] = fma(u.a[p], mul(x.a[p], f), dw[i].a[p]);
-            dw[i].b[p] = fma(u.b[p], mul(x.b[p], f), dw[i].b[p]);
-            u.a[p] = mul(f, fma(x.a[p], g, mul(u.a[p], w[i].a[p])));
-            u.b[p] = mul(f, fma(x.b[p], g, mul(u.b[p], w[i].b[p])));
+          for (int i = 0; i < UPT; ++i) {
+            const bool ks = un.k_side[i];
+            const float q0 = token ? (ks ? s[K + k] : s[k]) : lanes_sum(rs[k][i], lanes);
+            const float q1 = token ? (ks ? s[3 * K + k] : s[2 * K + k]) : lanes_sum(cf[k][i], lanes);
+            rs[k][i] = rsqrtf(q0 * un.inv[i] + a.eps);
+            cf[k][i] = rs[k][i] * rs[k][i] * q1 * un.inv[i];
           }
-        }
-        store16<T, L>(un.at(outs, a.out_stride, r + k, i), u, j, lanes, d);
       }
     }
-    if (RING) {
-      for (int k = 0; k < n; ++k) fetch();
-      us = us + n >= depth ? us + n - depth : us + n;
+    auto finish = [&](int k, int i, Unit& u, const Unit& x) {
+      if (normed) {
+        const float2 f = both(rs[k][i]), g = both(-cf[k][i]);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          dw[i].a[p] = fma(u.a[p], mul(x.a[p], f), dw[i].a[p]);
+          dw[i].b[p] = fma(u.b[p], mul(x.b[p], f), dw[i].b[p]);
+          u.a[p] = mul(f, fma(x.a[p], g, mul(u.a[p], w[i].a[p])));
+          u.b[p] = mul(f, fma(x.b[p], g, mul(u.b[p], w[i].b[p])));
+        }
+      }
+      if constexpr (KEEP) {
+        store16<T, L>(to, u, j, lanes, d);
+        to += un.step(a.out_stride, i);
+      } else {
+        store16<T, L>(un.at(outs, a.out_stride, r + k, i), u, j, lanes, d);
+      }
+    };
+    // absent heads stay out of dw whatever eps makes of their zeros
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (k < n && un.in[0]) finish(k, 0, uk[k], xk[k]);
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < n; ++k) {
+        Angles t;
+        get_angles(t, cs[buf] + (ago + k) * 16 * lanes, j, lanes);
+#pragma unroll
+        for (int i = 0; i < UPT; ++i) {
+          if (!un.in[i]) continue;
+          Unit u, x;
+          get_g(u, at[k], r + k, i, t);
+          if (normed) get_x(x, at[k], r + k, i);
+          finish(k, i, u, x);
+        }
+      }
+      next(n);
     }
-    buf ^= 1;
-    if (r + K < r1) angles<L, K>(a, tu, r + K, r1, cs[buf]);    // last read before this token's barrier
+    ago += K;
+    if (ago == kAhead) {         // the next ones, where those before these were: last read before this barrier
+      ago = 0;
+      buf ^= 1;
+      if (r + K < r1) angles<L>(a, tu, r + K, r1, cs[buf]);
+    }
   }
   if (RING) wait_async<0>();
   if (!normed || !a.part) return;
@@ -596,17 +658,23 @@ __global__ void __launch_bounds__(L::UPT == 2 ? 512 : 1024, 1) qk_bwd_kernel(con
 }
 
 // Adds the blocks' weight sums in a fixed order, in float64.
-__global__ void __launch_bounds__(1024) qk_reduce_kernel(const float* part, int blocks, int wq, int wk, float* dq,
+__global__ void __launch_bounds__(1024) qk_reduce_kernel(const float* __restrict__ part, int blocks, int wq, int wk, float* dq,
                                                          float* dk) {
   __shared__ double sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, width = wq + wk;
   const int col = blockIdx.x * 32 + lane;
   double s = 0.0;
-  if (col < width)
-    for (int b = warp; b < blocks; b += 32) s += (double)part[(long long)b * width + col];
+  for (int b = warp; b < blocks && col < width; b += 32 * 8) {      // a round of loads in flight together
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = b + 32 * i < blocks ? part[(long long)(b + 32 * i) * width + col] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += (double)v[i];
+  }
   sh[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && col < width) {
+#pragma unroll 8
     for (int v = 1; v < 32; ++v) s += sh[v][lane];
     float* o = col < wq ? dq : dk;
     if (o) o[col < wq ? col : col - wq] = (float)s;
@@ -614,17 +682,21 @@ __global__ void __launch_bounds__(1024) qk_reduce_kernel(const float* part, int 
 }
 
 // ----------------------------------------------------------------- launch --
-// Two units a thread, or four where 512 threads of two would not cover them.
-int units_per_thread(const QkArgs& a) { return (a.heads[0] + a.heads[1]) * a.lanes <= 1024 ? 2 : 4; }
-int block_threads(const QkArgs& a) {
-  const int upt = units_per_thread(a);
+// Two units a thread, or four where 512 threads of two would not cover them;
+// backward one where 512 threads of one do, so that a token's inputs stay in
+// registers.
+int units_per_thread(const QkArgs& a, bool back) {
+  const int units = (a.heads[0] + a.heads[1]) * a.lanes;
+  return back && units <= 512 ? 1 : (units <= 1024 ? 2 : 4);
+}
+int block_threads(const QkArgs& a, int upt) {
   return (((a.heads[0] + a.heads[1]) * a.lanes + upt - 1) / upt + 31) / 32 * 32;
 }
 
 constexpr int kSmemSm = 227 * 1024;
-constexpr int kStatic = sizeof(Turns) + sizeof(Scratch<4>) + 4 * SPADE_ROPE_MAX_PAIRS * sizeof(float2) + 1024 + 64;
+constexpr int kStatic = sizeof(Turns) + sizeof(Scratch<4>) + 4 * kAhead * SPADE_ROPE_MAX_PAIRS * sizeof(float) + 1024 + 64;
 
-// Blocks of an SM: by registers (96 a thread forward, 128 backward), and so
+// Blocks of an SM: by registers (`sm_threads` threads in all), and so
 // that `least` tokens a block fit in shared memory.
 int blocks_of(int threads, int sm_threads, size_t slot, int least) {
   int b = sm_threads / threads;
@@ -662,22 +734,27 @@ cudaError_t launch(K kernel, const QkArgs& a, int grid, int threads, int blocks,
 template <typename T, class L>
 cudaError_t run_fwd(const QkArgs& a, cudaStream_t s) {
   constexpr int K = 2;
-  const int threads = block_threads(a);
+  const int threads = block_threads(a, L::UPT);
   const size_t slot = (size_t)threads * L::UPT * 16 * sizeof(T);
   const int blocks = blocks_of(threads, 640, L::RING ? slot : 0, K);
   return launch(qk_fwd_kernel<T, L, K>, a, grid_of(a, blocks, K), threads, blocks, K, slot, L::RING, 0, s);
 }
 
+// Threads of an SM in the backward pass, by registers (96 or 128 a thread: five or four warps in each quarter of an SM).
+constexpr int bwd_sm_threads(int upt) { return upt == 1 ? 640 : 512; }
 // Blocks of an SM of the backward pass at most (bfloat16 rows).
-int bwd_blocks(const QkArgs& a) { return blocks_of(block_threads(a), 512, 0, 0); }
+int bwd_blocks(const QkArgs& a) {
+  const int upt = units_per_thread(a, true);
+  return blocks_of(block_threads(a, upt), bwd_sm_threads(upt), 0, 0);
+}
 
 template <typename T, class L>
 cudaError_t run_bwd(const QkArgs& a, cudaStream_t s) {
-  constexpr int K = sizeof(T) == 2 ? 2 : 1;
-  const int threads = block_threads(a);
+  constexpr int K = sizeof(T) == 2 && L::UPT > 1 ? 2 : 1;
+  const int threads = block_threads(a, L::UPT);
   const size_t slot = (size_t)threads * L::UPT * 16 * sizeof(T) * (a.norm != SPADE_QK_NORM_NONE ? 2 : 1);
   const size_t least = a.norm == SPADE_QK_NORM_HEAD ? (size_t)(threads / 32) * a.d * sizeof(float) : 0;
-  const int blocks = blocks_of(threads, 512, L::RING ? slot : 0, K == 1 ? 3 : K), grid = grid_of(a, blocks, K);
+  const int blocks = blocks_of(threads, bwd_sm_threads(L::UPT), L::RING ? slot : 0, K == 1 ? 3 : K), grid = grid_of(a, blocks, K);
   cudaError_t e = launch(qk_bwd_kernel<T, L, K>, a, grid, threads, blocks, K, slot, L::RING, least, s);
   if (e != cudaSuccess || !a.part) return e;
   const bool token = a.norm == SPADE_QK_NORM_TOKEN;
@@ -690,16 +767,19 @@ cudaError_t run_bwd(const QkArgs& a, cudaStream_t s) {
 // many channels need not fit in shared memory.
 template <typename T, int P, bool HALF, bool RING, bool WIDE>
 cudaError_t by_shape(const QkArgs& a, bool back, cudaStream_t s) {
-  if (units_per_thread(a) == 4) {
+  const int upt = units_per_thread(a, back);
+  if (upt == 4) {
     using L = Layout<P, HALF, false, false, 4>;
     return back ? run_bwd<T, L>(a, s) : run_fwd<T, L>(a, s);
   }
   if constexpr (WIDE) {
-    if (a.d == 16 * a.lanes && (a.heads[0] + a.heads[1]) * a.lanes == 2 * block_threads(a)) {
+    if (a.d == 16 * a.lanes && (a.heads[0] + a.heads[1]) * a.lanes == upt * block_threads(a, upt)) {
+      if (upt == 1) return run_bwd<T, Layout<P, HALF, true, RING, 1>>(a, s);
       using L = Layout<P, HALF, true, RING, 2>;
       return back ? run_bwd<T, L>(a, s) : run_fwd<T, L>(a, s);
     }
   }
+  if (upt == 1) return run_bwd<T, Layout<P, HALF, false, RING, 1>>(a, s);
   using L = Layout<P, HALF, false, RING, 2>;
   return back ? run_bwd<T, L>(a, s) : run_fwd<T, L>(a, s);
 }

@@ -20,19 +20,35 @@ __device__ __forceinline__ float param_at(const void* p, long long i, bool is_bf
   return is_bf16 ? __bfloat162float(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
+// Column sums of `n` units, `step` floats apart, that start at p: all loads of
+// a round are in flight together.
+template <int K0, int K1>
+__device__ __forceinline__ void sum_units(double (&s)[3], const float* __restrict__ p, long long n, long long step, int dim) {
+  constexpr int R = 8;
+  for (long long c = 0; c < n; c += R) {
+    float v[R][3];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = K0; k < K1; ++k) v[i][k] = c + i < n ? p[(c + i) * step + (long long)k * dim] : 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = K0; k < K1; ++k) s[k] += (double)v[i][k];
+  }
+}
+
+// K0, K1: the sums that the pass has, A and B with a norm, C with a residual.
+template <int K0, int K1>
 __global__ void __launch_bounds__(1024) row_reduce_kernel(const __grid_constant__ RowArgs a, int blocks) {
   __shared__ double sh[3][32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane, dim = a.dim;
+  const long long unit = 3LL * dim;
   const bool in = col < dim;
-  // the sums that the pass has: A and B with a norm, C with a residual
-  const int k0 = a.dh ? 0 : 2, k1 = a.dy ? 3 : 2;
   double wsum[3] = {0.0, 0.0, 0.0};
   if (a.chunks == 1) {
-    for (int b = warp; in && b < blocks; b += 32)
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (k >= k0 && k < k1) wsum[k] += (double)a.part[((long long)b * 3 + k) * dim + col];
+    if (in && warp < blocks) sum_units<K0, K1>(wsum, a.part + warp * unit + col, (blocks - warp + 31) / 32, 32 * unit, dim);
   } else {
     const bool sliced = a.groups < 16;        // every warp on every group
     const float w = in ? param_at(a.weight, col, a.param_bf16, 1.f) : 0.f;
@@ -42,18 +58,19 @@ __global__ void __launch_bounds__(1024) row_reduce_kernel(const __grid_constant_
       const long long g = sliced ? g0 : g0 + warp;
       double s[3] = {0.0, 0.0, 0.0};
       if (in && g < a.groups) {
-#pragma unroll 4
-        for (long long c = sliced ? warp : 0; c < a.chunks; c += sliced ? 32 : 1)
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-            if (k >= k0 && k < k1) s[k] += (double)a.part[((g * a.chunks + c) * 3 + k) * dim + col];
+        const float* p = a.part + g * a.chunks * unit + col;
+        if (!sliced) sum_units<K0, K1>(s, p, a.chunks, unit, dim);
+        else if (warp < a.chunks) sum_units<K0, K1>(s, p + warp * unit, (a.chunks - warp + 31) / 32, 32 * unit, dim);
       }
       if (sliced) {
-        for (int k = 0; k < 3; ++k) sh[k][warp][lane] = s[k];
+#pragma unroll
+        for (int k = K0; k < K1; ++k) sh[k][warp][lane] = s[k];
         __syncthreads();
         if (warp == 0)
+#pragma unroll 8
           for (int v = 1; v < 32; ++v)
-            for (int k = 0; k < 3; ++k) s[k] += sh[k][v][lane];
+#pragma unroll
+            for (int k = K0; k < K1; ++k) s[k] += sh[k][v][lane];
         __syncthreads();
       }
       if (in && g < a.groups && (!sliced || warp == 0)) {
@@ -67,10 +84,13 @@ __global__ void __launch_bounds__(1024) row_reduce_kernel(const __grid_constant_
       }
     }
   }
-  for (int k = 0; k < 3; ++k) sh[k][warp][lane] = wsum[k];
+  if (!a.dbias && !a.dweight && !a.dpost_weight) return;
+#pragma unroll
+  for (int k = K0; k < K1; ++k) sh[k][warp][lane] = wsum[k];
   __syncthreads();
-  if (warp < 3 && in) {
+  if (warp >= K0 && warp < K1 && in) {
     double s = 0.0;
+#pragma unroll 8
     for (int v = 0; v < 32; ++v) s += sh[warp][v][lane];
     float* out = warp == 0 ? a.dbias : (warp == 1 ? a.dweight : a.dpost_weight);
     if (out) out[col] = (float)s;
@@ -116,7 +136,10 @@ cudaError_t launch_row_bwd(const RowArgs& a, int grid, cudaStream_t s) {
   else e = a.branch_bf16 ? row_bwd<float, bf16>(a, grid, weights, s) : row_bwd<float, float>(a, grid, weights, s);
   if (e != cudaSuccess) return e;
   if (a.chunks > 1 || weights) {
-    row_reduce_kernel<<<(a.dim + 31) / 32, 1024, 0, s>>>(a, grid);
+    const int cols = (a.dim + 31) / 32;
+    if (a.dh && a.dy) row_reduce_kernel<0, 3><<<cols, 1024, 0, s>>>(a, grid);
+    else if (a.dh) row_reduce_kernel<0, 2><<<cols, 1024, 0, s>>>(a, grid);
+    else row_reduce_kernel<2, 3><<<cols, 1024, 0, s>>>(a, grid);
     e = cudaGetLastError();
   }
   return e;
