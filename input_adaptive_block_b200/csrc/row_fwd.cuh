@@ -18,13 +18,19 @@ using namespace rowpass;
 
 // POST: the branch has a norm (0 no, 1 yes, 2 as the call says).
 template <typename XT, typename BT, class L, int K, bool RES, bool NORM, int POST>
-__global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1) row_fwd_kernel(const __grid_constant__ RowArgs a, int depth) {
+__global__ void __maxnreg__(L::NV <= 2 ? 96 : 128) row_fwd_kernel(const __grid_constant__ RowArgs a, int depth) {
   constexpr int NV = L::NV;
   constexpr bool RING = L::RING;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ Shared<K> sh;
   const int dim = a.dim, nwarps = blockDim.x >> 5;
-  const long long r0 = a.rows * blockIdx.x / gridDim.x, r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
+  // With one modulation group the blocks take turns, K rows each, so that all of
+  // them read and write one stretch of memory; with several a block keeps to a
+  // run of rows and so to few groups.
+  const bool turns = a.groups == 1;
+  const long long tiles = (a.rows + K - 1) / K, hop = turns ? (gridDim.x - 1LL) * K : 0;      // rows of the others
+  const long long r0 = turns ? (long long)blockIdx.x * K : a.rows * blockIdx.x / gridDim.x;
+  const long long r1 = a.rows * (blockIdx.x + 1) / gridDim.x;
   Stream<XT, L> sx;
   Stream<BT, L> sy;
   sx.seek(a.x, a.x_stride, r0);
@@ -36,16 +42,24 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1) row_fwd_kernel(cons
   const uint32_t slot = sy.at + (RES ? slot_bytes(blockDim.x, NV, sizeof(BT)) : 0), ring_bytes = depth * slot;
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
 
-  int left = (int)(r1 - r0), to_copy = left;   // rows to use, and to copy
+  int left = (int)(r1 - r0);                   // rows to use, and to copy
+  if (turns) {
+    left = (int)((tiles - blockIdx.x + gridDim.x - 1) / gridDim.x) * K;
+    if ((tiles - 1) % gridDim.x == blockIdx.x) left -= (int)(tiles * K - a.rows);
+  }
+  int to_copy = left, of_turn = K;
   uint32_t fs = 0, us = 0;                     // slot of the next row to copy, of the next to use
   auto fetch = [&]() {
     if (to_copy > 0) {
       sx.fetch(ring_at + fs, dim);
-      sx.p += a.x_stride;
-      if (RES) {
-        sy.fetch(ring_at + fs, dim);
-        sy.p += a.y_stride;
+      if (RES) sy.fetch(ring_at + fs, dim);
+      long long step = 1;
+      if (--of_turn == 0) {
+        of_turn = K;
+        step += hop;
       }
+      sx.p += step * a.x_stride;
+      if (RES) sy.p += step * a.y_stride;
     }
     commit_async();
     --to_copy;
@@ -60,14 +74,14 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1) row_fwd_kernel(cons
   }
   count_columns<L>(sh, dim);
   int half = 0;
-  long long g = r0 / a.rows_per_group - 1;
+  long long g = turns ? -1 : r0 / a.rows_per_group - 1;
   int of_group = 0;              // rows until the next modulation group
   Eight gate[NV], times[NV], plus[NV];
   while (left > 0) {
     if (of_group == 0) {
       ++g;
       const long long end = (g + 1) * a.rows_per_group;
-      of_group = (int)((end < r1 ? end : r1) - (r1 - left));
+      of_group = turns ? left : (int)((end < r1 ? end : r1) - (r1 - left));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (RES) {
@@ -169,6 +183,12 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1) row_fwd_kernel(cons
     } else {
       for (int k = 0; k < n; ++k) rows(std::integral_constant<int, 1>());
     }
+    if (!RING) {
+      sx.p += hop * a.x_stride;
+      if (RES) sy.p += hop * a.y_stride;
+    }
+    if (RES) xo += hop * a.x_out_stride;
+    if (NORM) ho += hop * a.h_stride;
     left -= n;
     of_group -= n;
   }
@@ -185,7 +205,8 @@ cudaError_t run(const RowArgs& a, cudaStream_t s) {
   int blocks = 640 / threads < 16 ? 640 / threads : 16;
   if (blocks < 1) blocks = 1;
   const long long resident = (long long)num_sms() * blocks;
-  const int grid = (int)(a.rows < resident ? a.rows : resident);
+  const long long most = a.groups == 1 ? (a.rows + K - 1) / K : a.rows;
+  const int grid = (int)(most < resident ? most : resident);
   int depth = 0;
   size_t smem = 0;
   if (L::RING) {
@@ -213,23 +234,25 @@ cudaError_t by_op(const RowArgs& a, cudaStream_t s) {
   return run<XT, BT, L, false, true, 0>(a, s);
 }
 
-// The widest pieces have kernels for every length; rows above 8192 elements,
-// and rows above 5120 in narrower pieces, are read where they are used.
+// Sixteen columns a thread above 2560, so that two blocks share an SM and one
+// works while the other waits at a barrier.  Narrow pieces have kernels up to
+// 5120 elements; longer rows, and rows above 8192, are read where they are
+// used.
 template <typename XT, typename BT>
 cudaError_t by_width(const RowArgs& a, cudaStream_t s) {
   constexpr int P = sizeof(XT) == 2 ? 8 : 4;
   const int p = piece_of(a);
   const bool wide = p == P;
+  if (wide && a.dim <= 2560)
+    return a.dim % 256 == 0 ? by_op<XT, BT, Layout<P, true, true, 1>>(a, s) : by_op<XT, BT, Layout<P, false, true, 1>>(a, s);
+  if (wide && a.dim <= 8192)
+    return a.dim % 512 == 0 ? by_op<XT, BT, Layout<P, true, true, 2>>(a, s) : by_op<XT, BT, Layout<P, false, true, 2>>(a, s);
   if (a.dim <= 5120) {
-    const bool full = a.dim % 256 == 0;
-    if (wide) return full ? by_op<XT, BT, Layout<P, true, true, 1>>(a, s) : by_op<XT, BT, Layout<P, false, true, 1>>(a, s);
     if constexpr (sizeof(XT) == 2) {
       if (p > 1) return by_op<XT, BT, Layout<2, false, true, 1>>(a, s);
     }
     return by_op<XT, BT, Layout<1, false, sizeof(BT) == 4, 1>>(a, s);
   }
-  if (a.dim <= 8192 && wide)
-    return a.dim % 512 == 0 ? by_op<XT, BT, Layout<P, true, true, 2>>(a, s) : by_op<XT, BT, Layout<P, false, true, 2>>(a, s);
   return wide ? by_op<XT, BT, Layout<P, false, false, 4>>(a, s) : by_op<XT, BT, Layout<1, false, false, 4>>(a, s);
 }
 
