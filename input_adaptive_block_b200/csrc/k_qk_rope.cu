@@ -276,8 +276,14 @@ __device__ __forceinline__ void read_turns(Turns& tu, const QkArgs& a, float* cs
 }
 
 // ---------------------------------------------------------------- forward --
+// Fits in 96 registers: bfloat16 words from the ring.  What a thread holds of
+// float32 tokens, or of tokens it loads itself, does not.
+template <typename T, class L>
+constexpr bool lean() {
+  return sizeof(T) == 2 && L::RING;
+}
 template <typename T, class L, int K>
-__global__ void __launch_bounds__(L::UPT == 2 ? 640 : 1024, 1) qk_fwd_kernel(const __grid_constant__ QkArgs a, int depth) {
+__global__ void __maxnreg__(L::UPT == 4 ? 64 : (lean<T, L>() ? 96 : 128)) qk_fwd_kernel(const __grid_constant__ QkArgs a, int depth) {
   constexpr int UPT = L::UPT;
   constexpr bool RING = L::RING;
   extern __shared__ __align__(16) unsigned char ring[];
@@ -723,8 +729,8 @@ cudaError_t launch(K kernel, const QkArgs& a, int grid, int threads, int blocks,
     smem = depth * slot;
   }
   if (smem < least) smem = least;
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 32 * 1024) {        // one value for all launches: callers on other threads may be between theirs and this
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemSm - kStatic);
     if (e != cudaSuccess) return e;
   }
   kernel<<<grid, threads, smem, s>>>(a, depth);
@@ -736,7 +742,7 @@ cudaError_t run_fwd(const QkArgs& a, cudaStream_t s) {
   constexpr int K = 2;
   const int threads = block_threads(a, L::UPT);
   const size_t slot = (size_t)threads * L::UPT * 16 * sizeof(T);
-  const int blocks = blocks_of(threads, 640, L::RING ? slot : 0, K);
+  const int blocks = blocks_of(threads, lean<T, L>() ? 640 : 512, L::RING ? slot : 0, K);
   return launch(qk_fwd_kernel<T, L, K>, a, grid_of(a, blocks, K), threads, blocks, K, slot, L::RING, 0, s);
 }
 

@@ -135,7 +135,7 @@ cudaError_t launch_row_bwd(const RowArgs& a, int grid, cudaStream_t s) {
   if (a.x_bf16) e = row_bwd<bf16, bf16>(a, grid, weights, s);
   else e = a.branch_bf16 ? row_bwd<float, bf16>(a, grid, weights, s) : row_bwd<float, float>(a, grid, weights, s);
   if (e != cudaSuccess) return e;
-  if (a.chunks > 1 || weights) {
+  if (a.part) {
     const int cols = (a.dim + 31) / 32;
     if (a.dh && a.dy) row_reduce_kernel<0, 3><<<cols, 1024, 0, s>>>(a, grid);
     else if (a.dh) row_reduce_kernel<0, 2><<<cols, 1024, 0, s>>>(a, grid);

@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(L::NV == 1 ? 640 : 512, 1)
       left -= n;
     }
     if (a.chunks > 1) {
+      if (!a.part) continue;     // no gradient of a parameter is wanted
       float* p = a.part + u * 3 * dim;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -366,8 +367,9 @@ cudaError_t run(const RowArgs& a, int grid, bool weights, cudaStream_t s) {
     smem = depth * slot;
   }
   const auto kernel = row_bwd_kernel<XT, BT, L, K, RES, NORM, POST>;
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 32 * 1024) {        // one value for all launches: callers on other threads may be between theirs and this
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kSmemSm - 1024 - (int)sizeof(Shared<2 * K>));
     if (e != cudaSuccess) return e;
   }
   kernel<<<grid, threads, smem, s>>>(a, depth, weights);

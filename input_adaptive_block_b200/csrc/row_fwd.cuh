@@ -216,8 +216,9 @@ cudaError_t run(const RowArgs& a, cudaStream_t s) {
     depth = (int)(room / slot < kDepthMax ? room / slot : kDepthMax);
     if (rows < depth) depth = (int)(rows > K ? rows : K);
     smem = depth * slot;
-    if (smem > 32 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 32 * 1024) {      // one value for all launches: callers on other threads may be between theirs and this
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kSmemSm - 1024 - (int)sizeof(Shared<K>));
       if (e != cudaSuccess) return e;
     }
   }

@@ -85,6 +85,9 @@ QK = {
     "no_weights": _qk(60, norm="head", grid=(3, 4, 5), weights=False),
     "one_ladder": _qk(60, norm="none", grid=(3, 4, 5), shared=True, theta=1e6),
     "zero_eps": _qk(60, qh=5, kh=3, norm="head", grid=(3, 4, 5), eps=0.0),
+    "f32_interleaved": _qk(400, qh=8, kh=8, d=128, dtype=F32, norm="token", grid=(4, 10, 10)),
+    "f32_halves": _qk(400, qh=6, kh=2, d=64, pairs=(12, 10, 10), style="half", dtype=F32, norm="head", grid=(4, 10, 10)),
+    "many_tokens": _qk(3001, qh=12, kh=12, norm="token", grid=(5, 30, 30)),
     "many_rows": _qk(4321, qh=2, kh=1, d=64, pairs=(8, 12, 12), norm="head", grid=(5, 30, 30)),
 }
 
@@ -259,6 +262,10 @@ ROW = {
     "widest": _row(12, 16384, groups=4, params=ALL, post="rms", norm="layer"),
     "widest_odd": _row(12, 16383, groups=2, params=ALL, post="layer", norm="rms", x=F32),
     "between": _row(40, 5128, params=("gate", "scale", "shift")),
+    "many": _row(3001, 1536, params=ALL, post="rms", x=F32),
+    "many_of_five": _row(3005, 512, groups=5, params=ALL, post="layer"),
+    "long": _row(1207, 5120, params=("gate", "scale", "shift", "weight", "bias")),
+    "long_frames": _row(1212, 3584, groups=4, x=F32, b=F32),
     "far_from_zero": _row(64, 2048, x=F32, b=F32, half="norm", params=("scale", "shift"), mean=300.0),
 }
 
@@ -430,6 +437,55 @@ def test_other_stream_and_two_at_once():
     for g in got:
         for a, b in zip(want, g):
             assert (a is None and b is None) or torch.equal(a, b)
+
+
+def test_callers_on_several_host_threads():
+    """Calls of one kernel with rings of different sizes from host threads at
+    once, each on its own stream."""
+    import threading
+    cases = [RowCase(_row(rows, 5120, params=("scale", "shift"), half="norm")) for rows in (150, 700, 2400)]
+    want = [s.forward(None, None)[1] for s in cases]
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in cases], []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            for _ in range(50):
+                got[i].append(api.norm_modulate(cases[i].x.t, **cases[i].pre, stream=st))
+            st.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors, errors
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, x) for x in g)
+
+
+def test_no_parameter_gradients():
+    x, y = (torch.randn(300, 512, generator=_gen(i), device="cuda") for i in (1, 2))
+    ws = torch.full((api.row_workspace_bytes(300, 512),), 0xA5, dtype=torch.uint8, device="cuda")
+    g = api.gate_residual_norm_backward(x, y, x, y, workspace=ws)
+    assert bool((ws == 0xA5).all())
+    assert g.x.shape == g.y.shape == x.shape and g.gate is None and g.weight is None
+    ref = R.gate_residual_norm_backward(_b(x), _b(y), _b(x), _b(y), {n: None for n in PARAMS}, "layer", 1e-6, "none", 1e-6, 1.0)
+    check(g.x, ref["x"], "x")
+    check(g.y, ref["y"], "y")
+
+
+def test_same_tensor_for_q_and_k():
+    """One tensor as Q and as K, read twice, written to two outputs."""
+    x = torch.randn(60, 4, 128, generator=_gen(1), device="cuda").to(BF)
+    rope = api.rope_axes(128, (22, 21, 21))
+    q, k = api.qk_norm_rope(x, x, rope, grid=(3, 4, 5))
+    assert torch.equal(q, k)
+    with pytest.raises(RuntimeError):
+        api.qk_norm_rope(x, x, rope, grid=(3, 4, 5), q_out=x, k_out=x)
+    with pytest.raises(RuntimeError):
+        api.qk_norm_rope(x, x, rope, grid=(3, 4, 5), q_out=x)          # K would read what Q wrote
 
 
 def test_captured_and_replayed():
