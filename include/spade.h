@@ -355,8 +355,8 @@ spade_status spade_grouped_attn_host(const void* q_host, const void* k_host, con
  * stride at least the row's length; 0 = the row's length, packed), elements
  * of a row next to one another.  Pointers need the alignment of their type
  * only.  Rows on 16-byte boundaries, of a multiple of 16 (head channels) or 8
- * (dim) elements, are read and written 16 bytes at a time; all others run the
- * same kernels one element at a time.  An output may be the input of the same
+ * (dim) elements, are read and written 16 bytes at a time; others in pieces
+ * down to one element, as their length, strides and addresses allow.  An output may be the input of the same
  * row (same pointer and stride) where that is said; otherwise outputs overlap
  * nothing.  rows = 0 is allowed: nothing is read, parameter gradients become
  * zero.  Gradients of parameters are float32, added in a fixed order (the same

@@ -5,9 +5,16 @@
 //   x' = x + r * gate_g * P(y)          P: none, rms or layer norm * weight
 //   h  = (N(x') * w + b) * (1 + scale_g) + shift_g
 //
-// with g the row's modulation group.  A block walks a run of rows, K at a
-// time: their sums share a barrier, and the modulation stays in registers
-// while the group lasts.  Bound by memory: each row is read and written once.
+// with g the row's modulation group.  A block walks its rows K at a time:
+// their sums share a barrier, and the modulation stays in registers while the
+// group lasts.
+//
+// Bound by memory: each row is read and written once.  On 75600 rows of 5120
+// (bfloat16): h alone 251 us, 6.2 TB/s of the 6.55 that a copy reaches; x' and h
+// 491 to 550 us on different cards, 5.6 to 6.3 TB/s.  h alone took 1131 us with
+// one row to a block and a load when it was needed, 352 with the ring, 302 with
+// paired arithmetic and whole batches without per-row branches, 278 with the
+// moments merged without divisions, 251 with the blocks taking turns.
 #pragma once
 #include "row_pass.cuh"
 

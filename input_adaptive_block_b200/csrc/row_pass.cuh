@@ -7,7 +7,7 @@
 // every row's address allow (16 bytes; a single element in the worst case).
 // Rows that come in are copied ahead of their use into a ring of `depth` rows
 // (RING): every thread copies and reads its own columns only, so a ring needs
-// no barrier, and keeps some 100 KB in flight on an SM, which a load into
+// no barrier, and keeps some 100 KB in flight on an SM, which loads into
 // registers could not.  Without RING (pieces below 4 bytes, or rows of which
 // not two fit in shared memory) rows are read from global memory where they
 // are used.
