@@ -31,8 +31,11 @@
 // divisions (520), angles of four tokens at once (509).  Registers are capped
 // so that no value is spilled: with the ring in place the first-level cache is
 // nearly gone, and a spilled value is read from the second.  Backward, 32760
-// tokens of 2 x 12 heads, 148 us, 4.1 TB/s: the sums, the angles and the
-// addresses of a token are spread over fewer heads.
+// tokens of 2 x 12 heads, 143 us, 4.2 TB/s: the sums, the angles and the
+// addresses of a token are spread over fewer heads (150 us before warps of one
+// tensor summed for it alone and addresses took one multiply-add).
+#include <algorithm>
+
 #include "row_io.cuh"
 #include "spade_internal.cuh"
 
@@ -273,6 +276,21 @@ struct Units {
   }
 };
 
+// Two sums over the units of this thread's tensor, where every warp's units are
+// of one tensor: the warps from `first` to `last`.
+template <int M>
+__device__ __forceinline__ void side_sum(float (&v)[2], Scratch<M>& sh, int& half, int first, int last) {
+  const int lane = threadIdx.x & 31, sub = lane & 15;
+  float s = warp_sum_spread<2>(v);
+  float* b = reinterpret_cast<float*>(sh.v[half]) + (lane >> 4) * 33;
+  if (sub == 0) b[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = first + sub < last ? b[first + sub] : 0.f;      // 512 threads of one unit: 16 warps at most
+  s = spread_sum<2>(s);
+  half ^= 1;
+  spread_get<2>(v, s);
+}
+
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -434,6 +452,7 @@ __global__ void __maxnreg__(L::UPT == 4 ? 64 : (lean<T, L>() ? 96 : 128)) qk_fwd
 template <typename T, class L, int K>
 __global__ void __maxnreg__(L::UPT == 1 ? 96 : (L::UPT == 2 ? 128 : 64)) qk_bwd_kernel(const __grid_constant__ QkArgs a, int depth) {
   constexpr int UPT = L::UPT;
+  constexpr bool ONE_SIDE = UPT == 1 && L::FULL && K == 1;       // a warp's units are of Q or of K alone
   constexpr bool KEEP = UPT == 1;          // tokens stay in registers between the two passes over them
   constexpr bool RING = L::RING;
   extern __shared__ __align__(16) unsigned char ring[];
@@ -449,15 +468,23 @@ __global__ void __maxnreg__(L::UPT == 1 ? 96 : (L::UPT == 2 ? 128 : 64)) qk_bwd_
   const T* const xs[2] = {static_cast<const T*>(a.x[0]), static_cast<const T*>(a.x[1])};
   T* const outs[2] = {static_cast<T*>(a.out[0]), static_cast<T*>(a.out[1])};
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-  // with one unit: the next token to copy and the next to write (with more
-  // units their registers cost more than the products they save)
-  const T *from_g = nullptr, *from_x = nullptr;
-  T* to = nullptr;
+  // with one unit: its place in row 0 and the bytes to the next row (rows and
+  // strides below 2^32: one multiply-add makes an address)
+  const unsigned char *g0 = nullptr, *x0 = nullptr;
+  unsigned char* o0 = nullptr;
+  uint32_t g_step = 0, x_step = 0, o_step = 0;
   if constexpr (KEEP) {
-    from_g = un.at(gs, a.dout_stride, r0, 0);
-    from_x = un.at(xs, a.x_stride, r0, 0);
-    to = un.at(outs, a.out_stride, r0, 0);
+    const int t = un.k_side[0];
+    g0 = reinterpret_cast<const unsigned char*>(un.at(gs, a.dout_stride, 0, 0));
+    x0 = reinterpret_cast<const unsigned char*>(un.at(xs, a.x_stride, 0, 0));
+    o0 = reinterpret_cast<unsigned char*>(un.at(outs, a.out_stride, 0, 0));
+    g_step = (uint32_t)(a.dout_stride[t] * sizeof(T));
+    x_step = (uint32_t)(a.x_stride[t] * sizeof(T));
+    o_step = (uint32_t)(a.out_stride[t] * sizeof(T));
   }
+  auto row = [](const unsigned char* p, uint32_t step, long long r) {
+    return reinterpret_cast<const T*>(p + (unsigned long long)(uint32_t)r * step);
+  };
   long long fr = r0;
   int fs = 0, us = 0;
   auto fetch = [&]() {
@@ -468,12 +495,8 @@ __global__ void __maxnreg__(L::UPT == 1 ? 96 : (L::UPT == 2 ? 128 : 64)) qk_bwd_
           if (un.in[i]) {
             const uint32_t slot = ring_at + fs * un.slot;
             if constexpr (KEEP) {
-              fetch16<T, L>(slot + un.place(0, i), from_g, j, lanes, d);
-              from_g += un.step(a.dout_stride, i);
-              if (normed) {
-                fetch16<T, L>(slot + un.place(1, i), from_x, j, lanes, d);
-                from_x += un.step(a.x_stride, i);
-              }
+              fetch16<T, L>(slot + un.place(0, i), row(g0, g_step, fr), j, lanes, d);
+              if (normed) fetch16<T, L>(slot + un.place(1, i), row(x0, x_step, fr), j, lanes, d);
             } else {
               fetch16<T, L>(slot + un.place(0, i), un.at(gs, a.dout_stride, fr, i), j, lanes, d);
               if (normed) fetch16<T, L>(slot + un.place(1, i), un.at(xs, a.x_stride, fr, i), j, lanes, d);
@@ -497,6 +520,8 @@ __global__ void __maxnreg__(L::UPT == 1 ? 96 : (L::UPT == 2 ? 128 : 64)) qk_bwd_
   }
   read_turns(tu, a, cs[0], 4 * kAhead * SPADE_ROPE_MAX_PAIRS);
   angles<L>(a, tu, r0, r1, cs[0]);
+  const int q_warps = a.heads[0] * lanes / 32;
+  const int side_first = un.k_side[0] ? q_warps : 0, side_last = un.k_side[0] ? nwarps : q_warps;
   int half = 0, buf = 0, ago = 0;      // which angles, and how many of their tokens are done
   auto get_g = [&](Unit& v, const unsigned char* at, long long r, int i, const Angles& t) {
     if constexpr (RING) ring16<T, L>(v, at + un.place(0, i));
@@ -566,7 +591,18 @@ __global__ void __maxnreg__(L::UPT == 1 ? 96 : (L::UPT == 2 ? 128 : 64)) qk_bwd_
         }
       }
       if (KEEP) next(n);
-      if (token) block_sum(s, sums, half, nwarps);
+      if (ONE_SIDE) {
+        if (token && nwarps > 1) {
+          float both_sums[2] = {rs[0][0], cf[0][0]};
+          side_sum(both_sums, sums, half, side_first, side_last);
+          s[0] = s[K] = both_sums[0];
+          s[2 * K] = s[3 * K] = both_sums[1];
+        } else if (token) {
+          block_sum(s, sums, half, nwarps);
+        }
+      } else if (token) {
+        block_sum(s, sums, half, nwarps);
+      }
       if (normed) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -592,8 +628,7 @@ __global__ void __maxnreg__(L::UPT == 1 ? 96 : (L::UPT == 2 ? 128 : 64)) qk_bwd_
         }
       }
       if constexpr (KEEP) {
-        store16<T, L>(to, u, j, lanes, d);
-        to += un.step(a.out_stride, i);
+        store16<T, L>(const_cast<T*>(row(o0, o_step, r + k)), u, j, lanes, d);
       } else {
         store16<T, L>(un.at(outs, a.out_stride, r + k, i), u, j, lanes, d);
       }
@@ -702,9 +737,12 @@ __global__ void __launch_bounds__(1024) qk_reduce_kernel(const float* __restrict
 // Two units a thread, or four where 512 threads of two would not cover them;
 // backward one where 512 threads of one do, so that a token's inputs stay in
 // registers.
-int units_per_thread(const QkArgs& a, bool back) {
+int units_per_thread(const QkArgs& a, bool back, int size) {
   const int units = (a.heads[0] + a.heads[1]) * a.lanes;
-  return back && units <= 512 ? 1 : (units <= 1024 ? 2 : 4);
+  bool narrow = a.rows < 1LL << 32;          // addresses by a 32-bit row and step
+  for (int t = 0; t < 2; ++t)
+    for (long long st : {a.x_stride[t], a.dout_stride[t], a.out_stride[t]}) narrow = narrow && st * size < 1LL << 32;
+  return back && units <= 512 && narrow ? 1 : (units <= 1024 ? 2 : 4);
 }
 int block_threads(const QkArgs& a, int upt) {
   return (((a.heads[0] + a.heads[1]) * a.lanes + upt - 1) / upt + 31) / 32 * 32;
@@ -759,10 +797,13 @@ cudaError_t run_fwd(const QkArgs& a, cudaStream_t s) {
 
 // Threads of an SM in the backward pass, by registers (96 or 128 a thread: five or four warps in each quarter of an SM).
 constexpr int bwd_sm_threads(int upt) { return upt == 1 ? 640 : 512; }
-// Blocks of an SM of the backward pass at most (bfloat16 rows).
+// Blocks of an SM in the backward pass at most, whatever units a thread has.
 int bwd_blocks(const QkArgs& a) {
-  const int upt = units_per_thread(a, true);
-  return blocks_of(block_threads(a, upt), bwd_sm_threads(upt), 0, 0);
+  int most = 1;
+  for (int upt : {1, 2, 4})
+    if (block_threads(a, upt) <= (upt == 4 ? 1024 : 512))
+      most = std::max(most, blocks_of(block_threads(a, upt), bwd_sm_threads(upt), 0, 0));
+  return most;
 }
 
 template <typename T, class L>
@@ -784,14 +825,15 @@ cudaError_t run_bwd(const QkArgs& a, cudaStream_t s) {
 // many channels need not fit in shared memory.
 template <typename T, int P, bool HALF, bool RING, bool WIDE>
 cudaError_t by_shape(const QkArgs& a, bool back, cudaStream_t s) {
-  const int upt = units_per_thread(a, back);
+  const int upt = units_per_thread(a, back, sizeof(T));
   if (upt == 4) {
     using L = Layout<P, HALF, false, false, 4>;
     return back ? run_bwd<T, L>(a, s) : run_fwd<T, L>(a, s);
   }
   if constexpr (WIDE) {
     if (a.d == 16 * a.lanes && (a.heads[0] + a.heads[1]) * a.lanes == upt * block_threads(a, upt)) {
-      if (upt == 1) return run_bwd<T, Layout<P, HALF, true, RING, 1>>(a, s);
+      if (upt == 1 && a.heads[0] * a.lanes % 32 == 0) return run_bwd<T, Layout<P, HALF, true, RING, 1>>(a, s);
+      if (upt == 1) return run_bwd<T, Layout<P, HALF, false, RING, 1>>(a, s);
       using L = Layout<P, HALF, true, RING, 2>;
       return back ? run_bwd<T, L>(a, s) : run_fwd<T, L>(a, s);
     }
