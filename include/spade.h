@@ -360,7 +360,9 @@ spade_status spade_grouped_attn_host(const void* q_host, const void* k_host, con
  * row (same pointer and stride) where that is said; otherwise outputs overlap
  * nothing.  rows = 0 is allowed: nothing is read, parameter gradients become
  * zero.  Gradients of parameters are float32, added in a fixed order (the same
- * bits on every run of one device type), and overwritten, not accumulated. */
+ * bits on every run of one call on one device type), and overwritten, not
+ * accumulated.  A call owns its workspace until it has run: calls that may run
+ * at once, or graphs replayed at once, need one each. */
 
 /* A rotation: pair i turns by position[axis[i]] * freq[i] radians.  Axes are
  * 0 (t), 1 (y), 2 (x).  Pairs past `pairs` are left as they are (interleaved

@@ -328,6 +328,8 @@ def sics(q: torch.Tensor, k: torch.Tensor, candidates, workspace: Optional[torch
 
 
 # ---- row passes around the attention ----------------------------------------
+# Plain calls on plain tensors: autograd records none of them, the _backward
+# calls are its counterpart.
 def rope_axes(d: int, pairs: Sequence[int], theta=10000.0, scale=1.0, style: str = "interleaved",
               shared_ladder: bool = False) -> SpadeRope:
     """The rotation of heads of d channels over the axes (t, y, x): pairs[a]

@@ -8,9 +8,8 @@
 // Rows that come in are copied ahead of their use into a ring of `depth` rows
 // (RING): every thread copies and reads its own columns only, so a ring needs
 // no barrier, and keeps some 100 KB in flight on an SM, which loads into
-// registers could not.  Without RING (pieces below 4 bytes, or rows of which
-// not two fit in shared memory) rows are read from global memory where they
-// are used.
+// registers could not.  Without RING (pieces below 4 bytes, and long rows: see
+// the launch code) rows are read from global memory where they are used.
 #pragma once
 #include "row_io.cuh"
 #include "spade_internal.cuh"

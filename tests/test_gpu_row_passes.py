@@ -439,6 +439,41 @@ def test_other_stream_and_two_at_once():
             assert (a is None and b is None) or torch.equal(a, b)
 
 
+@pytest.mark.parametrize("stride", [1_200_000_000, 2_200_000_000])
+def test_offsets_past_32_bits(stride):
+    """Rows so far apart that their offsets pass 32 bits, in elements and (the
+    wider stride) in bytes of a single step."""
+    def rows_of(shape, gen):
+        n = int(np.prod(shape[1:]))
+        buf = torch.empty(2 * stride + n, dtype=BF, device="cuda")
+        t = buf.as_strided(shape, (stride, *(int(np.prod(shape[i + 1:])) for i in range(1, len(shape)))))
+        t.copy_(torch.randn(shape, generator=gen, device="cuda"))
+        return t
+
+    gen = _gen(11)
+    x = rows_of((3, 256), gen)
+    y = torch.randn(3, 256, generator=gen, device="cuda").to(BF)
+    near = x.contiguous()
+    for a, b in zip(api.gate_residual_norm(x, y), api.gate_residual_norm(near, y)):
+        assert torch.equal(a, b)
+    for a, b in zip(api.gate_residual_norm_backward(x, y, x, y)[:2], api.gate_residual_norm_backward(near, y, near, y)[:2]):
+        assert torch.equal(a, b)
+    api.norm_modulate(near, out=x)
+    assert torch.equal(x, api.norm_modulate(near))
+    del x
+    q = rows_of((3, 2, 128), gen)
+    w, rope = torch.rand(256, generator=gen, device="cuda"), api.rope_axes(128, (22, 21, 21))
+    kw = dict(grid=(1, 1, 3), norm="token", q_weight=w, k_weight=w)
+    near = q.contiguous()
+    k = torch.randn(3, 2, 128, generator=gen, device="cuda").to(BF)
+    for a, b in zip(api.qk_norm_rope(q, k, rope, **kw), api.qk_norm_rope(near, k, rope, **kw)):
+        assert torch.equal(a, b)
+    far, want = api.qk_norm_rope_backward(q, k, q, k, rope, **kw), api.qk_norm_rope_backward(near, k, near, k, rope, **kw)
+    half = 2.0 ** -8          # another split of the heads over threads: the sums' order, so a rounding, may differ
+    for a, b in zip(far, want):
+        assert (a.float() - b.float()).abs().max() <= 2.01 * half * b.float().abs().max()
+
+
 def test_callers_on_several_host_threads():
     """Calls of one kernel with rings of different sizes from host threads at
     once, each on its own stream."""
