@@ -715,6 +715,7 @@ __global__ void __launch_bounds__(1024) qk_reduce_kernel(const float* __restrict
   __shared__ double sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, width = wq + wk;
   const int col = blockIdx.x * 32 + lane;
+  cudaGridDependencySynchronize();
   double s = 0.0;
   for (int b = warp; b < blocks && col < width; b += 32 * 8) {      // a round of loads in flight together
     float v[8];
@@ -817,8 +818,7 @@ cudaError_t run_bwd(const QkArgs& a, cudaStream_t s) {
   if (e != cudaSuccess || !a.part) return e;
   const bool token = a.norm == SPADE_QK_NORM_TOKEN;
   const int wq = token ? a.heads[0] * a.d : a.d, wk = token ? a.heads[1] * a.d : a.d;
-  qk_reduce_kernel<<<(wq + wk + 31) / 32, 1024, 0, s>>>(a.part, grid, wq, wk, a.dweight[0], a.dweight[1]);
-  return cudaGetLastError();
+  return launch_behind(qk_reduce_kernel, (wq + wk + 31) / 32, 1024, s, a.part, grid, wq, wk, a.dweight[0], a.dweight[1]);
 }
 
 // Threads of four units read tokens where they are used: two tokens of so

@@ -24,7 +24,7 @@ __device__ __forceinline__ float param_at(const void* p, long long i, bool is_bf
 // a round are in flight together.
 template <int K0, int K1>
 __device__ __forceinline__ void sum_units(double (&s)[3], const float* __restrict__ p, long long n, long long step, int dim) {
-  constexpr int R = 8;
+  constexpr int R = K1 - K0 == 1 ? 16 : 8;
   for (long long c = 0; c < n; c += R) {
     float v[R][3];
 #pragma unroll
@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(1024) row_reduce_kernel(const __grid_constant_
   const int col = blockIdx.x * 32 + lane, dim = a.dim;
   const long long unit = 3LL * dim;
   const bool in = col < dim;
+  cudaGridDependencySynchronize();
   double wsum[3] = {0.0, 0.0, 0.0};
   if (a.chunks == 1) {
     if (in && warp < blocks) sum_units<K0, K1>(wsum, a.part + warp * unit + col, (blocks - warp + 31) / 32, 32 * unit, dim);
@@ -137,10 +138,8 @@ cudaError_t launch_row_bwd(const RowArgs& a, int grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (a.part) {
     const int cols = (a.dim + 31) / 32;
-    if (a.dh && a.dy) row_reduce_kernel<0, 3><<<cols, 1024, 0, s>>>(a, grid);
-    else if (a.dh) row_reduce_kernel<0, 2><<<cols, 1024, 0, s>>>(a, grid);
-    else row_reduce_kernel<2, 3><<<cols, 1024, 0, s>>>(a, grid);
-    e = cudaGetLastError();
+    const auto kernel = a.dh && a.dy ? row_reduce_kernel<0, 3> : (a.dh ? row_reduce_kernel<0, 2> : row_reduce_kernel<2, 3>);
+    e = launch_behind(kernel, cols, 1024, s, a, grid);
   }
   return e;
 }

@@ -194,5 +194,21 @@ __device__ __forceinline__ void block_sum(float (&v)[N], Scratch<M>& sh, int& ha
   spread_get<N>(v, s);
 }
 
+// Launches a kernel that follows another in its stream and waits for it with
+// cudaGridDependencySynchronize(): its launch is prepared while the other runs.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), int grid, int threads, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 }  // namespace rowio
 }  // namespace spade

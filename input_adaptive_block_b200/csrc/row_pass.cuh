@@ -113,14 +113,15 @@ struct Stream {
   }
   // Columns past the row's end read as zero.
   __device__ __forceinline__ void clear(unsigned char* slot, int dim) const {
-    if (L::FULL) return;
+    if constexpr (!L::FULL) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = column<L>(i, e);
-        if (!inside<L>(c, dim)) reinterpret_cast<T*>(slot + at)[c] = T(0.f);
-      }
+        for (int e = 0; e < 8; ++e) {
+          const int c = column<L>(i, e);
+          if (!inside<L>(c, dim)) reinterpret_cast<T*>(slot + at)[c] = T(0.f);
+        }
+    }
   }
   // The row in a slot, or `ahead` elements past the next one in memory.
   __device__ __forceinline__ void get(Eight& v, const unsigned char* slot, long long ahead, int i, int dim) const {
