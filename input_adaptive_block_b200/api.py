@@ -7,6 +7,7 @@ arithmetic happens in its CUDA kernels.  PyTorch provides memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
@@ -413,8 +414,9 @@ def _strided(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dt
     packed inside and may lie any distance apart."""
     if t is None:
         return None, 0
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda and t.get_device() == like.get_device():
-        return t.data_ptr(), 0
+    if t is like or (t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device()):
+        if t.is_contiguous() and t.dtype is dtype and t.is_cuda:
+            return t.data_ptr(), 0
     _on_gpu(t, name, like)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
@@ -465,14 +467,29 @@ def _param_dtype(params) -> torch.dtype:
 
 
 def _scratch(workspace, need: int, like: torch.Tensor) -> Tuple[Optional[int], int, Optional[torch.Tensor]]:
+    """(pointer, bytes, tensor) of the caller's workspace or of a new one."""
     if workspace is None:
         if not need:
             return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return workspace.data_ptr(), need, workspace
     _on_gpu(workspace, "workspace", like)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+@functools.lru_cache(maxsize=1024)
+def _row_scratch_bytes(device: int, rows: int, dim: int, groups: int) -> int:
+    """Of sizes and the current device alone, which is `device`."""
+    desc = SpadeRowDesc(rows=rows, groups=groups, dim=dim)
+    return int(_lib.load().spade_row_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _qk_scratch_bytes(device: int, rows: int, q_heads: int, k_heads: int, d: int, norm: int) -> int:
+    desc = SpadeQkDesc(rows=rows, q_heads=q_heads, k_heads=k_heads, d=d, norm=norm)
+    return int(_lib.load().spade_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(desc)))
 
 
 def _code(table, key, name: str) -> int:
@@ -577,7 +594,9 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
             dk, ko, desc.k_out_stride = _output(dk, "dk", dk_out, ks, dt)
         dqw, dkw = (None if w is None else _new(w, w.shape, torch.float32) for w in (q_weight, k_weight))
         lib = _lib.load()
-        need = int(lib.spade_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(desc))) if dqw is not None or dkw is not None else 0
+        need = 0
+        if dqw is not None or dkw is not None:
+            need = _qk_scratch_bytes(like.get_device(), rows, desc.q_heads, desc.k_heads, d, desc.norm)
         wp, wn, workspace = _scratch(workspace, need, like)
         check(lib.spade_qk_norm_rope_bwd(ctypes.byref(desc), ctypes.byref(rope), pos, gq, gk, qp, kp, qw, kw, qo, ko,
                                          dqw.data_ptr() if dqw is not None else None,
@@ -679,7 +698,7 @@ def norm_modulate_backward(dout: torch.Tensor, x: torch.Tensor, weight: Optional
         dx, dp, desc.dx_stride = _output(dx, "dx", x, x.shape, x.dtype)
         out, grads = _row_grads(given, x)
         lib = _lib.load()
-        wp, wn, workspace = _scratch(workspace, int(lib.spade_row_bwd_workspace_bytes(ctypes.byref(desc))), x)
+        wp, wn, workspace = _scratch(workspace, _row_scratch_bytes(x.get_device(), desc.rows, desc.dim, desc.groups), x)
         check(lib.spade_norm_modulate_bwd(ctypes.byref(desc), ctypes.byref(params), hp, rp, xp, dp, ctypes.byref(grads),
                                           wp, wn, s), "spade_norm_modulate_bwd")
     return RowGrads(x=dx, y=None, **out)
@@ -716,7 +735,7 @@ def gate_residual_backward(dout: torch.Tensor, y: torch.Tensor, gate: Optional[t
         dy, dp, desc.dy_stride = _output(dy, "dy", y, dout.shape, y.dtype)
         out, grads = _row_grads(given, dout)
         lib = _lib.load()
-        wp, wn, workspace = _scratch(workspace, int(lib.spade_row_bwd_workspace_bytes(ctypes.byref(desc))), dout)
+        wp, wn, workspace = _scratch(workspace, _row_scratch_bytes(dout.get_device(), desc.rows, desc.dim, desc.groups), dout)
         check(lib.spade_gate_residual_bwd(ctypes.byref(desc), ctypes.byref(params), gp, yp, dp, ctypes.byref(grads), wp,
                                           wn, s), "spade_gate_residual_bwd")
     return RowGrads(x=dout, y=dy, **out)
@@ -766,7 +785,7 @@ def gate_residual_norm_backward(dx_out: Optional[torch.Tensor], dout: torch.Tens
         dy, dyp, desc.dy_stride = _output(dy, "dy", y, x.shape, y.dtype)
         out, grads = _row_grads(given, x)
         lib = _lib.load()
-        wp, wn, workspace = _scratch(workspace, int(lib.spade_row_bwd_workspace_bytes(ctypes.byref(desc))), x)
+        wp, wn, workspace = _scratch(workspace, _row_scratch_bytes(x.get_device(), desc.rows, desc.dim, desc.groups), x)
         check(lib.spade_gate_residual_norm_bwd(ctypes.byref(desc), ctypes.byref(params), gp, hp, xp, yp, dxp, dyp,
                                                ctypes.byref(grads), wp, wn, s), "spade_gate_residual_norm_bwd")
     return RowGrads(x=dx, y=dy, **out)
