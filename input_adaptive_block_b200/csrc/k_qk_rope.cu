@@ -31,7 +31,7 @@
 // divisions (520), angles of four tokens at once (509).  Registers are capped
 // so that no value is spilled: with the ring in place the first-level cache is
 // nearly gone, and a spilled value is read from the second.  Backward, 32760
-// tokens of 2 x 12 heads, 143 us, 4.2 TB/s: the sums, the angles and the
+// tokens of 2 x 12 heads, 141 us, 4.3 TB/s: the sums, the angles and the
 // addresses of a token are spread over fewer heads (150 us before warps of one
 // tensor summed for it alone and addresses took one multiply-add).
 #include <algorithm>
