@@ -414,8 +414,8 @@ def _strided(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dt
     packed inside and may lie any distance apart."""
     if t is None:
         return None, 0
-    if t is like or (t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device()):
-        if t.is_contiguous() and t.dtype is dtype and t.is_cuda:
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        if t is like or (t.is_cuda and t.get_device() == like.get_device()):      # like is on a GPU
             return t.data_ptr(), 0
     _on_gpu(t, name, like)
     if tuple(t.shape) != tuple(shape):

@@ -1,0 +1,16 @@
+"""Calls of the row passes that a user may make by mistake or at the edge of
+what is allowed, through the public entry points."""
+import pytest
+import torch
+
+from input_adaptive_block_b200 import api
+
+pytestmark = pytest.mark.gpu
+
+
+def test_one_tensor_as_gradient_of_q_and_as_k():
+    rope = api.rope_axes(64, (8, 12, 12))
+    few, many = (torch.zeros(6, h, 64, dtype=torch.bfloat16, device="cuda") for h in (2, 5))
+    for a, b in ((few, many), (many, few)):
+        with pytest.raises(ValueError):
+            api.qk_norm_rope_backward(a, b, a, a, rope, grid=(1, 2, 3), norm="head")
