@@ -480,10 +480,17 @@ def _scratch(workspace, need: int, like: torch.Tensor) -> Tuple[Optional[int], i
 
 
 @functools.lru_cache(maxsize=1024)
-def _row_scratch_bytes(device: int, rows: int, dim: int, groups: int) -> int:
+def _row_plan_bytes(device: int, rows: int, dim: int, groups: int) -> int:
     """Of sizes and the current device alone, which is `device`."""
     desc = SpadeRowDesc(rows=rows, groups=groups, dim=dim)
     return int(_lib.load().spade_row_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def _row_scratch_bytes(like: torch.Tensor, desc: SpadeRowDesc, given) -> int:
+    """Of a backward row pass on like's device: none without a parameter."""
+    if all(t is None for t in given.values()):
+        return 0
+    return _row_plan_bytes(like.get_device(), desc.rows, desc.dim, desc.groups)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -698,7 +705,7 @@ def norm_modulate_backward(dout: torch.Tensor, x: torch.Tensor, weight: Optional
         dx, dp, desc.dx_stride = _output(dx, "dx", x, x.shape, x.dtype)
         out, grads = _row_grads(given, x)
         lib = _lib.load()
-        wp, wn, workspace = _scratch(workspace, _row_scratch_bytes(x.get_device(), desc.rows, desc.dim, desc.groups), x)
+        wp, wn, workspace = _scratch(workspace, _row_scratch_bytes(x, desc, given), x)
         check(lib.spade_norm_modulate_bwd(ctypes.byref(desc), ctypes.byref(params), hp, rp, xp, dp, ctypes.byref(grads),
                                           wp, wn, s), "spade_norm_modulate_bwd")
     return RowGrads(x=dx, y=None, **out)
@@ -735,7 +742,7 @@ def gate_residual_backward(dout: torch.Tensor, y: torch.Tensor, gate: Optional[t
         dy, dp, desc.dy_stride = _output(dy, "dy", y, dout.shape, y.dtype)
         out, grads = _row_grads(given, dout)
         lib = _lib.load()
-        wp, wn, workspace = _scratch(workspace, _row_scratch_bytes(dout.get_device(), desc.rows, desc.dim, desc.groups), dout)
+        wp, wn, workspace = _scratch(workspace, _row_scratch_bytes(dout, desc, given), dout)
         check(lib.spade_gate_residual_bwd(ctypes.byref(desc), ctypes.byref(params), gp, yp, dp, ctypes.byref(grads), wp,
                                           wn, s), "spade_gate_residual_bwd")
     return RowGrads(x=dout, y=dy, **out)
@@ -785,7 +792,7 @@ def gate_residual_norm_backward(dx_out: Optional[torch.Tensor], dout: torch.Tens
         dy, dyp, desc.dy_stride = _output(dy, "dy", y, x.shape, y.dtype)
         out, grads = _row_grads(given, x)
         lib = _lib.load()
-        wp, wn, workspace = _scratch(workspace, _row_scratch_bytes(x.get_device(), desc.rows, desc.dim, desc.groups), x)
+        wp, wn, workspace = _scratch(workspace, _row_scratch_bytes(x, desc, given), x)
         check(lib.spade_gate_residual_norm_bwd(ctypes.byref(desc), ctypes.byref(params), gp, hp, xp, yp, dxp, dyp,
                                                ctypes.byref(grads), wp, wn, s), "spade_gate_residual_norm_bwd")
     return RowGrads(x=dx, y=dy, **out)

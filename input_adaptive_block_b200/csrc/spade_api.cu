@@ -739,10 +739,11 @@ spade_status run_row_bwd(const spade_row_desc* desc, const spade_row_params* par
   const bool weights = a.dweight || a.dbias || a.dpost_weight;
   const RowPlan plan = plan_row_bwd(a.rows, a.groups, a.dim, weights);
   a.chunks = plan.chunks;
-  if ((st = check_scratch(workspace, ws_bytes, plan.floats * sizeof(float))) != SPADE_OK) return st;
-  const bool sums = weights || a.dgate || a.dscale || a.dshift;      // else the workspace stays as it is
-  a.part = plan.floats && sums ? static_cast<float*>(workspace) : nullptr;
-  rs.add("workspace", a.part, 1, 0, (long long)(plan.floats * sizeof(float)), true);
+  const bool sums = weights || a.dgate || a.dscale || a.dshift;      // else no column sum leaves its block
+  const size_t need = sums ? plan.floats * sizeof(float) : 0;
+  if ((st = check_scratch(workspace, ws_bytes, need)) != SPADE_OK) return st;
+  a.part = need ? static_cast<float*>(workspace) : nullptr;
+  rs.add("workspace", a.part, 1, 0, (long long)need, true);
   if ((st = check_rows(a, ops, 6, rs)) != SPADE_OK) return st;
   const cudaError_t e = launch_row_bwd(a, plan.grid, s);
   return e == cudaSuccess ? SPADE_OK : cuda_fail(e, where);

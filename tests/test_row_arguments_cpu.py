@@ -1,10 +1,14 @@
 """What the Python side of the row passes does with its arguments, on a machine
 without a GPU: tensors are stand-ins that are asked for their shape, type,
 strides and address and never read."""
+import ctypes
+
 import pytest
 import torch
 
-from input_adaptive_block_b200 import api
+from input_adaptive_block_b200 import _lib, api
+from input_adaptive_block_b200._lib import (SPADE_ERR_INVALID, SPADE_ERR_WORKSPACE, SpadeRowDesc, SpadeRowGrads,
+                                            SpadeRowParams)
 
 
 class Standin:
@@ -45,3 +49,18 @@ def test_one_tensor_in_two_roles_has_its_shape_checked():
                 api._strided(other, "k", t, shape, torch.bfloat16)
     with pytest.raises(TypeError):
         api._strided(t, "k", t, (10, 2, 64), torch.float32)
+
+
+def test_scratch_is_for_parameter_gradients():
+    """A backward call that wants none needs no workspace: the next check (dx
+    over part of dh) refuses it, not the one of the workspace."""
+    base, lib = 1 << 40, _lib.load()
+    desc = SpadeRowDesc(rows=600, groups=1, dim=256, norm=2, eps=1e-6)
+    for grads, want in ((SpadeRowGrads(), SPADE_ERR_INVALID), (SpadeRowGrads(bias=9 * base), SPADE_ERR_WORKSPACE)):
+        got = lib.spade_norm_modulate_bwd(ctypes.byref(desc), ctypes.byref(SpadeRowParams()), base, None, 2 * base,
+                                          base + 64, ctypes.byref(grads), None, 0, None)
+        assert got == want, lib.spade_last_error_message()
+    x, w = Standin(600, 256), Standin(256)
+    none = dict.fromkeys(("gate", "post_weight", "weight", "bias", "scale", "shift"))
+    assert api._row_scratch_bytes(x, desc, none) == 0
+    assert api._row_scratch_bytes(x, desc, {**none, "bias": w}) == api.row_workspace_bytes(600, 256) > 0
