@@ -636,13 +636,16 @@ def _row_call(like, x_dtype, branch_dtype, norm="none", eps=0.0, post_norm="none
                 raise ValueError("gate, scale and shift must have one number of groups")
             groups = g
             p, stride = _strided(t if t.dim() == 2 else t.unsqueeze(0), name, like, (g, dim), pdt)
+            if not g:
+                p = None
             if stride:
                 strides = strides or {}
                 strides[name] = stride
         else:
             p = _vector(t, name, like, dim, pdt)
         setattr(params, name, p)
-    groups = 1 if groups is None else groups
+    if groups is None or groups == rows == 0:      # none, or one for each of no rows
+        groups = 1
     if groups < 1 or rows % groups:
         raise ValueError(f"{rows} rows in {groups} groups")
     desc = SpadeRowDesc(rows, groups, dim, dtype_code(x_dtype), dtype_code(branch_dtype), dtype_code(pdt),

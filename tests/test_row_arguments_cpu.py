@@ -64,3 +64,12 @@ def test_scratch_is_for_parameter_gradients():
     none = dict.fromkeys(("gate", "post_weight", "weight", "bias", "scale", "shift"))
     assert api._row_scratch_bytes(x, desc, none) == 0
     assert api._row_scratch_bytes(x, desc, {**none, "bias": w}) == api.row_workspace_bytes(600, 256) > 0
+
+
+def test_modulation_per_row_of_no_rows():
+    """No rows and a modulation for each of them: no groups, nothing to do."""
+    x, m = Standin(0, 64), Standin(0, 64)
+    desc, params, _ = api._row_call(x, x.dtype, x.dtype, "layer", 1e-6, scale=m, shift=m)
+    assert (desc.rows, desc.groups) == (0, 1) and not params.scale and not params.shift
+    with pytest.raises(ValueError):
+        api._row_call(Standin(5, 64), x.dtype, x.dtype, "layer", 1e-6, scale=m)
