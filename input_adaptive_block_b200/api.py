@@ -331,6 +331,14 @@ def sics(q: torch.Tensor, k: torch.Tensor, candidates, workspace: Optional[torch
 # ---- row passes around the attention ----------------------------------------
 # Plain calls on plain tensors: autograd records none of them, the _backward
 # calls are its counterpart.
+def _fits(bits: int, *numbers: int) -> None:
+    """ctypes cuts what a field cannot hold to its low bits without a word."""
+    top = 1 << (bits - 1)
+    for n in numbers:
+        if not -top <= n < top:
+            raise ValueError(f"{n} does not fit {bits} bits")
+
+
 def rope_axes(d: int, pairs: Sequence[int], theta=10000.0, scale=1.0, style: str = "interleaved",
               shared_ladder: bool = False) -> SpadeRope:
     """The rotation of heads of d channels over the axes (t, y, x): pairs[a]
@@ -344,6 +352,7 @@ def rope_axes(d: int, pairs: Sequence[int], theta=10000.0, scale=1.0, style: str
         raise ValueError("pairs, theta and scale have one entry per axis (t, y, x)")
     if 2 * sum(int(p) for p in pairs) > d:
         raise ValueError(f"{sum(pairs)} pairs in heads of {d} channels")
+    _fits(32, *(int(p) for p in pairs))
     rope = SpadeRope()
     check(_lib.load().spade_rope_axes(ctypes.byref(rope), (ctypes.c_int32 * 3)(*[int(p) for p in pairs]),
                                       (ctypes.c_double * 3)(*th), (ctypes.c_double * 3)(*sc),
@@ -513,9 +522,12 @@ def _qk_desc(q, k, q_weight, k_weight, grid, positions, token_offset, text_token
     if like.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != like.shape[0] or k.shape[2] != like.shape[2])):
         raise ValueError("q and k are [rows, heads, d]")
     rows, _, d = like.shape
+    q_heads, k_heads = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    text_tokens, token_offset = int(text_tokens), int(token_offset)
+    _fits(32, q_heads, k_heads, d)
+    _fits(64, text_tokens, token_offset)
     wdt = _param_dtype((q_weight, k_weight))
-    desc = SpadeQkDesc(rows, int(text_tokens), int(token_offset), 0, 0, 0, 0 if q is None else q.shape[1],
-                       0 if k is None else k.shape[1], d, dtype_code(like.dtype), dtype_code(wdt),
+    desc = SpadeQkDesc(rows, text_tokens, token_offset, 0, 0, 0, q_heads, k_heads, d, dtype_code(like.dtype), dtype_code(wdt),
                        _code(QK_NORM, norm, "norm"), eps)
     pos = None
     if positions is not None:
@@ -530,7 +542,9 @@ def _qk_desc(q, k, q_weight, k_weight, grid, positions, token_offset, text_token
     elif grid is not None:
         g = grid if isinstance(grid, SpadeGeom) else None
         t = (g.T, g.H, g.W) if g is not None else (grid.as_tuple() if hasattr(grid, "as_tuple") else tuple(grid))
-        desc.T, desc.H, desc.W = int(t[0]), int(t[1]), int(t[2])
+        extents = int(t[0]), int(t[1]), int(t[2])
+        _fits(32, *extents)
+        desc.T, desc.H, desc.W = extents
     elif rows > text_tokens:
         raise ValueError("neither positions nor a grid")
     per = lambda t: 0 if t is None else (t.shape[1] * d if norm == "token" else d)  # noqa: E731
@@ -569,6 +583,8 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: Spa
 
 def qk_norm_rope_workspace_bytes(rows: int, q_heads: int, k_heads: int, d: int, norm: str) -> int:
     """Scratch of qk_norm_rope_backward on the current device."""
+    _fits(64, rows)
+    _fits(32, q_heads, k_heads, d)
     desc = SpadeQkDesc(rows=rows, q_heads=q_heads, k_heads=k_heads, d=d, norm=_code(QK_NORM, norm, "norm"))
     return int(_lib.load().spade_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(desc)))
 
@@ -622,6 +638,7 @@ def _row_call(like, x_dtype, branch_dtype, norm="none", eps=0.0, post_norm="none
     if like.dim() != 2:
         raise ValueError("rows are [rows, dim]")
     rows, dim = like.shape
+    _fits(32, dim)
     params, strides, groups = SpadeRowParams(), None, None
     given = {"gate": gate, "post_weight": post_weight, "weight": weight, "bias": bias, "scale": scale, "shift": shift}
     pdt = _param_dtype(given.values())
@@ -670,6 +687,8 @@ def _row_grads(given, like):
 def row_workspace_bytes(rows: int, dim: int, groups: int = 1) -> int:
     """Scratch of norm_modulate_backward, gate_residual_backward and
     gate_residual_norm_backward on the current device."""
+    _fits(64, rows, groups)
+    _fits(32, dim)
     desc = SpadeRowDesc(rows=rows, groups=groups, dim=dim)
     return int(_lib.load().spade_row_bwd_workspace_bytes(ctypes.byref(desc)))
 

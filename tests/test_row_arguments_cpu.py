@@ -73,3 +73,25 @@ def test_modulation_per_row_of_no_rows():
     assert (desc.rows, desc.groups) == (0, 1) and not params.scale and not params.shift
     with pytest.raises(ValueError):
         api._row_call(Standin(5, 64), x.dtype, x.dtype, "layer", 1e-6, scale=m)
+
+
+WIDE = 1 << 32
+
+
+@pytest.mark.parametrize("call", [
+    lambda x: api._row_call(Standin(1, WIDE + 64), x.dtype, x.dtype, "layer", 1e-6),
+    lambda x: api._qk_desc(Standin(6, 1, WIDE + 64), None, None, None, (1, 2, 3), None, 0, 0, "none", 1e-6),
+    lambda x: api._qk_desc(x, Standin(6, WIDE + 2, 64), None, None, (1, 2, 3), None, 0, 0, "none", 1e-6),
+    lambda x: api._qk_desc(x, None, None, None, (1, WIDE + 2, 3), None, 0, 0, "none", 1e-6),
+    lambda x: api._qk_desc(x, None, None, None, (1, 2, 3 - WIDE), None, 0, 0, "none", 1e-6),
+    lambda x: api._qk_desc(x, None, None, None, (1, 2, 3), None, WIDE * WIDE, 0, "none", 1e-6),
+    lambda x: api._qk_desc(x, None, None, None, (1, 2, 3), None, 0, WIDE * WIDE, "none", 1e-6),
+    lambda x: api.rope_axes(8 * WIDE, (WIDE, 1, 1)),
+    lambda x: api.row_workspace_bytes(600, WIDE + 256),
+    lambda x: api.row_workspace_bytes(600, 256, WIDE * WIDE + 1),
+    lambda x: api.qk_norm_rope_workspace_bytes(600, 4, WIDE + 4, 128, "head"),
+])
+def test_numbers_wider_than_the_descriptor(call):
+    """Refused, not cut to their low bits."""
+    with pytest.raises(ValueError, match="does not fit"):
+        call(Standin(6, 2, 64))
