@@ -421,7 +421,7 @@ spade_status spade_qk_norm_rope(const spade_qk_desc* desc, const spade_rope* rop
  * call's inputs (unused, may be NULL, without a norm).  dq_weight, dk_weight:
  * float32, or NULL.  dq / dk may be dq_out / dk_out.  workspace: device scratch of
  * spade_qk_norm_rope_bwd_workspace_bytes() bytes (0 without a norm), asked for
- * with the device of the call current; none (NULL, 0) where no gradient of a
+ * with the device of the call current; it may be NULL where no gradient of a
  * weight is wanted. */
 size_t spade_qk_norm_rope_bwd_workspace_bytes(const spade_qk_desc* desc);
 spade_status spade_qk_norm_rope_bwd(const spade_qk_desc* desc, const spade_rope* rope, const int32_t* positions,
@@ -471,8 +471,9 @@ spade_status spade_gate_residual_norm(const spade_row_desc* desc, const spade_ro
                                       const void* y, void* x_out, void* h, spade_stream_t stream);
 
 /* Gradients.  workspace: device scratch of spade_row_bwd_workspace_bytes()
- * bytes, asked for with the device of the call current; none (NULL, 0) where no
- * gradient of a parameter is wanted.
+ * bytes, asked for with the device of the call current; it may be NULL where no
+ * gradient of a parameter is wanted (one that is given has that size all the
+ * same, and stays as it is).
  * spade_norm_modulate_bwd: dx = dres + the gradient through the norm; dres
  * (stride dx_out_stride) is a gradient that reaches x by another way, or NULL.
  * spade_gate_residual_bwd: dy from dx_out (the gradient of x is dx_out).

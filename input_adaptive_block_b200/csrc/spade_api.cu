@@ -740,9 +740,9 @@ spade_status run_row_bwd(const spade_row_desc* desc, const spade_row_params* par
   const RowPlan plan = plan_row_bwd(a.rows, a.groups, a.dim, weights);
   a.chunks = plan.chunks;
   const bool sums = weights || a.dgate || a.dscale || a.dshift;      // else no column sum leaves its block
-  const size_t need = sums ? plan.floats * sizeof(float) : 0;
+  const size_t need = sums || workspace ? plan.floats * sizeof(float) : 0;      // one that is given is whole
   if ((st = check_scratch(workspace, ws_bytes, need)) != SPADE_OK) return st;
-  a.part = need ? static_cast<float*>(workspace) : nullptr;
+  a.part = need && sums ? static_cast<float*>(workspace) : nullptr;
   rs.add("workspace", a.part, 1, 0, (long long)need, true);
   if ((st = check_rows(a, ops, 6, rs)) != SPADE_OK) return st;
   const cudaError_t e = launch_row_bwd(a, plan.grid, s);

@@ -56,9 +56,10 @@ def test_scratch_is_for_parameter_gradients():
     over part of dh) refuses it, not the one of the workspace."""
     base, lib = 1 << 40, _lib.load()
     desc = SpadeRowDesc(rows=600, groups=1, dim=256, norm=2, eps=1e-6)
-    for grads, want in ((SpadeRowGrads(), SPADE_ERR_INVALID), (SpadeRowGrads(bias=9 * base), SPADE_ERR_WORKSPACE)):
+    for grads, ws, want in ((SpadeRowGrads(), None, SPADE_ERR_INVALID), (SpadeRowGrads(bias=9 * base), None, SPADE_ERR_WORKSPACE),
+                            (SpadeRowGrads(), 8 * base, SPADE_ERR_WORKSPACE)):       # one that is given has its size
         got = lib.spade_norm_modulate_bwd(ctypes.byref(desc), ctypes.byref(SpadeRowParams()), base, None, 2 * base,
-                                          base + 64, ctypes.byref(grads), None, 0, None)
+                                          base + 64, ctypes.byref(grads), ws, 16 if ws else 0, None)
         assert got == want, lib.spade_last_error_message()
     x, w = Standin(600, 256), Standin(256)
     none = dict.fromkeys(("gate", "post_weight", "weight", "bias", "scale", "shift"))
