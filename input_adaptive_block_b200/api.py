@@ -497,9 +497,10 @@ def _row_plan_bytes(device: int, rows: int, dim: int, groups: int) -> int:
 
 def _row_scratch_bytes(like: torch.Tensor, desc: SpadeRowDesc, given) -> int:
     """Of a backward row pass on like's device: none without a parameter."""
-    if all(t is None for t in given.values()):
-        return 0
-    return _row_plan_bytes(like.get_device(), desc.rows, desc.dim, desc.groups)
+    for t in given.values():
+        if t is not None:
+            return _row_plan_bytes(like.get_device(), desc.rows, desc.dim, desc.groups)
+    return 0
 
 
 @functools.lru_cache(maxsize=1024)
@@ -524,8 +525,9 @@ def _qk_desc(q, k, q_weight, k_weight, grid, positions, token_offset, text_token
     rows, _, d = like.shape
     q_heads, k_heads = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
     text_tokens, token_offset = int(text_tokens), int(token_offset)
-    _fits(32, q_heads, k_heads, d)
-    _fits(64, text_tokens, token_offset)
+    if (q_heads | k_heads | d) >> 31 or (text_tokens | token_offset) >> 63:
+        _fits(32, q_heads, k_heads, d)
+        _fits(64, text_tokens, token_offset)
     wdt = _param_dtype((q_weight, k_weight))
     desc = SpadeQkDesc(rows, text_tokens, token_offset, 0, 0, 0, q_heads, k_heads, d, dtype_code(like.dtype), dtype_code(wdt),
                        _code(QK_NORM, norm, "norm"), eps)
@@ -542,9 +544,10 @@ def _qk_desc(q, k, q_weight, k_weight, grid, positions, token_offset, text_token
     elif grid is not None:
         g = grid if isinstance(grid, SpadeGeom) else None
         t = (g.T, g.H, g.W) if g is not None else (grid.as_tuple() if hasattr(grid, "as_tuple") else tuple(grid))
-        extents = int(t[0]), int(t[1]), int(t[2])
-        _fits(32, *extents)
-        desc.T, desc.H, desc.W = extents
+        T, H, W = int(t[0]), int(t[1]), int(t[2])
+        if (T | H | W) >> 31:
+            _fits(32, T, H, W)
+        desc.T, desc.H, desc.W = T, H, W
     elif rows > text_tokens:
         raise ValueError("neither positions nor a grid")
     per = lambda t: 0 if t is None else (t.shape[1] * d if norm == "token" else d)  # noqa: E731
@@ -638,7 +641,8 @@ def _row_call(like, x_dtype, branch_dtype, norm="none", eps=0.0, post_norm="none
     if like.dim() != 2:
         raise ValueError("rows are [rows, dim]")
     rows, dim = like.shape
-    _fits(32, dim)
+    if dim >> 31:
+        _fits(32, dim)
     params, strides, groups = SpadeRowParams(), None, None
     given = {"gate": gate, "post_weight": post_weight, "weight": weight, "bias": bias, "scale": scale, "shift": shift}
     pdt = _param_dtype(given.values())
