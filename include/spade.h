@@ -355,8 +355,10 @@ spade_status spade_grouped_attn_host(const void* q_host, const void* k_host, con
  * stride at least the row's length; 0 = the row's length, packed), elements
  * of a row next to one another.  Pointers need the alignment of their type
  * only.  Rows on 16-byte boundaries, of a multiple of 16 (head channels) or 8
- * (dim) elements, are read and written 16 bytes at a time; others in pieces
- * down to one element, as their length, strides and addresses allow.  An output may be the input of the same
+ * (dim) elements, are read and written 16 bytes at a time (a bfloat16 branch
+ * beside a float32 stream 8); others in pieces of two bfloat16 elements or of
+ * one, as their length, strides and addresses allow, and much slower.  An output
+ * may be the input of the same
  * row (same pointer and stride) where that is said; otherwise outputs overlap
  * nothing.  rows = 0 is allowed: nothing is read, parameter gradients become
  * zero.  Gradients of parameters are float32, added in a fixed order (the same
@@ -365,8 +367,9 @@ spade_status spade_grouped_attn_host(const void* q_host, const void* k_host, con
  * at once, or graphs replayed at once, need one each. */
 
 /* A rotation: pair i turns by position[axis[i]] * freq[i] radians.  Axes are
- * 0 (t), 1 (y), 2 (x).  Pairs past `pairs` are left as they are (interleaved
- * style only). */
+ * 0 (t), 1 (y), 2 (x).  Pairs past `pairs` (interleaved style only), and those of
+ * text rows, turn by zero: finite values stay as they are; an infinity or NaN
+ * reaches the pair's other channel as it does in any pair. */
 #define SPADE_ROPE_MAX_PAIRS 128
 typedef enum {
   SPADE_ROPE_INTERLEAVED = 0,  /* pair i = channels 2i, 2i + 1      */

@@ -569,7 +569,8 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: Spa
     text_tokens rows are text and not rotated; or at positions[r] (int32
     [rows, 3], t y x).  q_out / k_out: where the results go (q and k
     themselves are allowed), packed tensors by default.  Returns (q_out,
-    k_out)."""
+    k_out).  Plain results: autograd records nothing, whatever the inputs
+    require; qk_norm_rope_backward gives the gradients."""
     desc, like, pos, (qw, kw) = _qk_desc(q, k, q_weight, k_weight, grid, positions, token_offset, text_tokens, norm, eps)
     with _On(like, stream) as s:
         dt, qo, ko = like.dtype, None, None
@@ -705,7 +706,9 @@ def norm_modulate(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
     shift, each parameter optional.  x [rows, dim]; weight, bias [dim]; scale,
     shift [groups, dim] (or [dim]): the rows fall into `groups` equal runs
     (frames, samples, or single tokens).  norm: "layer" or "rms".  The result
-    is out, or a new tensor of out_dtype (x's by default)."""
+    is out, or a new tensor of out_dtype (x's by default).  Autograd records
+    nothing, whatever the inputs require; norm_modulate_backward gives the
+    gradients."""
     odt = out.dtype if out is not None else (out_dtype or x.dtype)
     desc, params, _ = _row_call(x, x.dtype, odt, norm, eps, weight=weight, bias=bias, scale=scale, shift=shift)
     with _On(x, stream) as s:
@@ -742,7 +745,9 @@ def gate_residual(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor]
                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The update that ends a block: x + residual_scale * gate *
     (post_norm(y) * post_weight).  x, y [rows, dim]; gate [groups, dim] or
-    [dim].  out: where the sum goes (x itself is allowed)."""
+    [dim].  out: where the sum goes (x itself is allowed).  Autograd records
+    nothing, whatever the inputs require; gate_residual_backward gives the
+    gradients."""
     desc, params, _ = _row_call(x, x.dtype, y.dtype, post_norm=post_norm, post_eps=post_eps,
                                 residual_scale=residual_scale, gate=gate, post_weight=post_weight)
     with _On(x, stream) as s:
@@ -783,7 +788,9 @@ def gate_residual_norm(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Te
                        stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """gate_residual and the norm_modulate of the block that follows, in one
     pass: returns (x_out, out), out of y's dtype, taken of the sum before it
-    is rounded to x's.  x_out may be x, out may be y."""
+    is rounded to x's.  x_out may be x, out may be y.  gate, scale and shift
+    have one number of groups.  Autograd records nothing, whatever the inputs
+    require; gate_residual_norm_backward gives the gradients."""
     desc, params, _ = _row_call(x, x.dtype, y.dtype, norm, eps, post_norm, post_eps, residual_scale, gate, post_weight,
                                 weight, bias, scale, shift)
     with _On(x, stream) as s:

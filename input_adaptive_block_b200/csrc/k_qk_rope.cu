@@ -23,17 +23,30 @@
 // by the thread that uses them (no barrier); a block takes K tokens at a time,
 // whose sums share one barrier.
 //
-// Bound by memory, and close to it by instruction issue: 20 to 30 instructions
-// an element cost 1314 us on 75600 tokens of 2 x 40 heads of 128 channels
-// (bfloat16, norm over the token), 8 an element 509 us, 6.1 TB/s of the 6.55
-// that a copy reaches.  What brought it there: the ring (709), paired float32
-// arithmetic (586), no checks where heads and threads divide evenly and no
-// divisions (520), angles of four tokens at once (509).  Registers are capped
-// so that no value is spilled: with the ring in place the first-level cache is
-// nearly gone, and a spilled value is read from the second.  Backward, 32760
-// tokens of 2 x 12 heads, 141 us, 4.3 TB/s: the sums, the angles and the
-// addresses of a token are spread over fewer heads (150 us before warps of one
-// tensor summed for it alone and addresses took one multiply-add).
+// Forward, bound by memory: 506 to 547 us on different cards for 75600 tokens
+// of 2 x 40 heads of 128 channels (bfloat16, norm over the token), 5.7 to 6.1
+// TB/s of the 6.55 that a copy reaches, at 14 instructions an element and 61 %
+// of the issue slots; float32 967 us, 6.4 TB/s.  Steps, on one card: 1314 us
+// with loads where they are needed, the ring (709), paired float32 arithmetic
+// (586), no checks where heads and threads divide evenly and no divisions (520),
+// angles of four tokens at once (509).
+//
+// Backward, bound by waits: 139 to 143 us for 32760 tokens of 2 x 12 heads
+// (bfloat16), 4.3 TB/s, with a quarter of an SM's warps at work, one token to a
+// barrier and 56 % of the issue slots used (150 us before warps of one tensor
+// summed for it alone and addresses took one multiply-add).  With two units a
+// thread (513 to 1024 units) a token is read from the ring and turned twice:
+// 1237 us for 75600 tokens of 2 x 40 heads, 3.8 TB/s.
+//
+// Registers are capped by what the blocks of an SM leave a thread.  The kernels
+// of 16-byte pieces with one or two units spill nothing or up to 16 bytes; with
+// narrower pieces 0 to 232 bytes.  Those of four units have 64 registers, spill
+// 0.9 to 2.2 KB and read every token twice, when it is needed: 2567 us forward
+// and 3657 backward for 32760 tokens of 2 x 40 heads of 160 channels, ten times
+// their bytes.  Narrow pieces cost as their accesses do (32760 tokens
+// of 2 x 12 heads, forward): 145 us in pieces of two, 301 in single elements.
+// Few heads leave threads of a warp without a unit: 114 us for 75600 tokens of
+// 2 x 2 heads, five times their bytes.
 #include <algorithm>
 
 #include "row_io.cuh"

@@ -15,13 +15,26 @@
 // ring where a later step needs them, which costs fewer registers than keeping
 // them.
 //
-// Bound by memory and, nearly as much, by instruction issue.  On 75600 rows of
-// 5120 (bfloat16), x' and h: 770 to 820 us, 5.7 to 6.0 TB/s of the 6.55 that a
-// copy reaches (2571 with one row to a block, 1680 with the ring, 1010 paired,
-// 880 with the moments merged without divisions, 819 without a spill).  On
-// 32760 rows of 1536 in 21 groups, h alone, float32 stream: 107 us, 4.7 TB/s.
-// Copying whole rows in bulk, one thread for all, was slower (930 us: its state
-// takes registers or calls), and so were chunks that take turns (800).
+// The sums of a unit, and of a block's units where it has several of one
+// launch, run in float32, over some 2 rows / SMs additions at most; from there
+// on in float64.
+//
+// With x' and h bound by memory: 75600 rows of 5120 (bfloat16) take 760 to 863 us
+// on different cards, 5.4 to 6.1 TB/s of the 6.55 that a copy reaches (steps on
+// one card: 2571 with one row to a block, 1680 with the ring, 1010 paired, 880
+// with the moments merged without divisions, 819 without a spill).  h alone moves
+// fewer bytes for the same statistics and waits: for shared memory, which dh is
+// read from twice, and at barriers, with a quarter of an SM's warps at work and
+// 56 % of the issue slots used.  32760 rows of 1536 in 21 groups, float32 stream,
+// 106 to 109 us, 4.7 TB/s; bfloat16 stream 102 us, 3.0 TB/s; 75600 rows of 5120,
+// bfloat16, 578 us, 4.0 TB/s.  Copying whole rows in bulk, one thread for all,
+// was slower (930 us: its state takes registers or calls), and so were chunks
+// that take turns (800).
+//
+// Rows above 8192 columns, and narrow pieces above 5120, spill 0.2 to 1.1 KB with
+// a norm: 723 us for x' and h of 8192 x 16384, three times their bytes (16384 x
+// 8192: 295 us, 1.2 times).  32760 rows of 1540 bfloat16 (h alone) in pieces of
+// two 145 us, of 1537 in single elements 244, where 1536 take 46 of bytes.
 #pragma once
 #include "row_pass.cuh"
 

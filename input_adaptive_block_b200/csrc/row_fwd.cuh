@@ -10,11 +10,17 @@
 // group lasts.
 //
 // Bound by memory: each row is read and written once.  On 75600 rows of 5120
-// (bfloat16): h alone 251 us, 6.2 TB/s of the 6.55 that a copy reaches; x' and h
-// 491 to 550 us on different cards, 5.6 to 6.3 TB/s.  h alone took 1131 us with
-// one row to a block and a load when it was needed, 352 with the ring, 302 with
-// paired arithmetic and whole batches without per-row branches, 278 with the
-// moments merged without divisions, 251 with the blocks taking turns.
+// (bfloat16), different cards: h alone 250 to 276 us, 5.6 to 6.2 TB/s of the 6.55
+// that a copy reaches; x' and h 491 to 552 us, 5.6 to 6.3 TB/s.  Steps of h alone,
+// on one card: 1131 us with one row to a block and a load when it was needed, 352
+// with the ring, 302 with paired arithmetic and whole batches without per-row
+// branches, 278 with the moments merged without divisions, 251 with the blocks
+// taking turns.
+//
+// With one modulation a row the batch is one row and its parameters are loaded
+// where they are used: 162 us for h of 32760 rows of 1536 (float32 stream), 1.5
+// times their bytes.  Narrow pieces: h of 32760 rows of 1540 bfloat16 in pieces
+// of two 71 us, of 1537 in single elements 108, where 1536 take 31 of bytes.
 #pragma once
 #include "row_pass.cuh"
 
@@ -245,7 +251,8 @@ cudaError_t by_op(const RowArgs& a, cudaStream_t s) {
 // Sixteen columns a thread above 2560, so that two blocks share an SM and one
 // works while the other waits at a barrier.  Narrow pieces have kernels up to
 // 5120 elements; longer rows, and rows above 8192, are read where they are
-// used.
+// used (x' and h of 16384 x 8192 bfloat16 193 us, 1.2 times their bytes; of
+// 8192 x 16384, as many bytes, 294).
 template <typename XT, typename BT>
 cudaError_t by_width(const RowArgs& a, cudaStream_t s) {
   constexpr int P = sizeof(XT) == 2 ? 8 : 4;

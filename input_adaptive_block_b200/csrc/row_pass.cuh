@@ -3,8 +3,10 @@
 //
 // A block holds K rows at a time and a thread the same columns of each: NV
 // times eight, in pieces of P neighbours that lie P * blockDim apart, so that a
-// warp's access is contiguous.  P is the widest piece that the row length and
-// every row's address allow (16 bytes; a single element in the worst case).
+// warp's access is contiguous.  P is eight bfloat16 elements where stream and
+// branch are bfloat16, four where the stream is float32 (a bfloat16 branch then
+// moves 8 bytes at a time), if the row length and every row's address allow it;
+// else two (bfloat16 stream), else a single element.
 // Rows that come in are copied ahead of their use into a ring of `depth` rows
 // (RING): every thread copies and reads its own columns only, so a ring needs
 // no barrier, and keeps some 100 KB in flight on an SM, which loads into
